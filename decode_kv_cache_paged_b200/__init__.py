@@ -41,21 +41,25 @@ KVC_ERR_UNSUPPORTED = 8
 
 KVC_BF16 = 0
 KVC_F32 = 1
+KVC_INT4 = 2
 
 KVC_SEL_RANDOM = 0
 KVC_SEL_RANDOM_SHARED = 1
 KVC_SEL_BEACON = 2
 KVC_SEL_BEACON_TRIGGER = 3
+KVC_SEL_ATTENTION = 4
 
 KVC_OPT_BEACON_SCORE_IMPL = 0
 KVC_OPT_BEACON_UPDATE_IMPL = 1
+KVC_OPT_RECENT_TOKENS = 2
 
 KVC_COMPACT_ORDERED = 0
 KVC_COMPACT_HOLE_FILL = 1
 COMPACTIONS = {"ordered": KVC_COMPACT_ORDERED, "hole_fill": KVC_COMPACT_HOLE_FILL}
 
 SELECTORS = {"random": KVC_SEL_RANDOM, "random_shared": KVC_SEL_RANDOM_SHARED,
-             "beacon": KVC_SEL_BEACON, "beacon_trigger": KVC_SEL_BEACON_TRIGGER}
+             "beacon": KVC_SEL_BEACON, "beacon_trigger": KVC_SEL_BEACON_TRIGGER,
+             "attention": KVC_SEL_ATTENTION}
 
 
 class kvc_config(ctypes.Structure):
@@ -86,6 +90,10 @@ class kvc_round_options(ctypes.Structure):
                 ("compaction", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class kvc_attention_options(ctypes.Structure):
+    _fields_ = [("accumulate", ctypes.c_int32), ("decay", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)]
+
+
 class kvc_view(ctypes.Structure):
     _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
@@ -111,6 +119,9 @@ _SIGS = {
     "kvc_compress_ex": (_i32, [_P, _i32, _P, _u64, ctypes.POINTER(kvc_round_options), _P,
                                ctypes.POINTER(kvc_round_stats)]),
     "kvc_decode_attention": (_i32, [_P, _i32, _i32, _P, ctypes.c_float, _P, _P, _P]),
+    "kvc_decode_attention_ex": (_i32, [_P, _i32, _i32, _P, ctypes.c_float, ctypes.POINTER(kvc_attention_options),
+                                       _P, _P, _P]),
+    "kvc_bind_weights": (_i32, [_P, _P, ctypes.c_size_t]),
     "kvc_gather_view": (_i32, [_P, ctypes.POINTER(kvc_view)]),
     "kvc_get_lengths": (_i32, [_P, _P, _P]),
     "kvc_gather_dense": (_i32, [_P, _i32, _i32, _i32, _i32, _P, _P, _P]),
@@ -144,6 +155,8 @@ def _check(status: int, ctx=None):
 
 def _dtype_code(dtype) -> int:
     import torch
+    if dtype == "int4":
+        return KVC_INT4
     if dtype == torch.bfloat16:
         return KVC_BF16
     if dtype == torch.float32:
@@ -174,22 +187,31 @@ class ContextSpec:
 
 
 class Context:
-    """One eviction context over torch-allocated pools and workspace."""
+    """One eviction context over torch-allocated pools and workspace.
+
+    ``dtype`` is the cache's: torch.bfloat16, torch.float32, or "int4" for the
+    4-bit cache (KVC_INT4), whose K, V and queries are bfloat16 and whose pools
+    hold the coded rows as bytes.  ``self.dtype`` is the type of the K, V and
+    query tensors; ``self.weights`` the tracked attention weights or None."""
 
     def __init__(self, spec: ContextSpec, dtype=None, device="cuda", stream=None):
         import torch
         dtype = dtype or torch.bfloat16
         self.spec = spec
-        self.dtype = dtype
+        self.int4 = dtype == "int4"
+        self.dtype = torch.bfloat16 if self.int4 else dtype
         self.device = torch.device(device)
+        self.weights = None
         self.cfg = spec.config(_dtype_code(dtype))
         ws_bytes = kvc_workspace_bytes(ctypes.byref(self.cfg))
         if ws_bytes == 0:
             raise KvcError(KVC_ERR_INVALID_ARG, "invalid context configuration")
         Hq = self.cfg.num_q_heads
-        shape = (spec.num_layers, spec.num_pages, spec.num_kv_heads, 16, spec.head_dim)
-        self.k_pool = torch.empty(shape, dtype=dtype, device=self.device)
-        self.v_pool = torch.empty(shape, dtype=dtype, device=self.device)
+        shape = (spec.num_layers, spec.num_pages, spec.num_kv_heads, 16,
+                 spec.head_dim // 2 + 16 if self.int4 else spec.head_dim)
+        pool_dtype = torch.uint8 if self.int4 else dtype
+        self.k_pool = torch.empty(shape, dtype=pool_dtype, device=self.device)
+        self.v_pool = torch.empty(shape, dtype=pool_dtype, device=self.device)
         self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
         self.stream = stream or torch.cuda.current_stream(self.device)
         self.handle = ctypes.c_void_p()
@@ -251,11 +273,33 @@ class Context:
                                ctypes.byref(st) if stats else None), self.handle)
         return st.as_dict() if stats else None
 
+    def track_weights(self, weights=None):
+        """kvc_bind_weights: tracks the rows' accumulated attention weights from 0
+        on, in ``weights`` or in a new tensor, float32 [layers, pages, Hkv, 16] as
+        the position map.  Returns the tensor, which is also ``self.weights``."""
+        import torch
+        s = self.spec
+        shape = (s.num_layers, s.num_pages, s.num_kv_heads, 16)
+        if weights is None:
+            weights = torch.empty(shape, dtype=torch.float32, device=self.device)
+        if tuple(weights.shape) != shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+            raise ValueError(f"weights must be contiguous float32 of shape {shape}")
+        _check(kvc_bind_weights(self.handle, _ptr(weights), weights.numel() * 4), self.handle)
+        self.weights = weights
+        return weights
+
+    def untrack_weights(self):
+        """Stops the tracking (kvc_bind_weights with no buffer)."""
+        _check(kvc_bind_weights(self.handle, None, 0), self.handle)
+        self.weights = None
+
     def decode_attention(self, q, layer_begin: int = 0, out=None, lse=None, scale: float = 0.0,
-                         with_lse: bool = True, timed: bool = False):
-        """kvc_decode_attention for q [layer_count, R, Hq, d] (cache dtype, on the
-        context's device).  Returns (out, lse) float32 tensors, plus the device
-        time in ms when timed."""
+                         with_lse: bool = True, timed: bool = False, accumulate: bool = False,
+                         decay: float = 1.0):
+        """kvc_decode_attention_ex for q [layer_count, R, Hq, d] (the context's
+        dtype, on its device).  Returns (out, lse) float32 tensors, plus the device
+        time in ms when timed.  With accumulate each cached row's tracked weight
+        becomes decay * weight + its attention weight of this step."""
         import torch
         s = self.spec
         if q.dim() != 4 or q.shape[1:] != (s.num_requests, s.num_q_heads, s.head_dim) or q.dtype != self.dtype:
@@ -268,8 +312,10 @@ class Context:
         if lse is None and with_lse:
             lse = torch.empty((lc, s.num_requests, s.num_q_heads), dtype=torch.float32, device=self.device)
         ms = ctypes.c_float(0.0)
-        _check(kvc_decode_attention(self.handle, int(layer_begin), int(lc), _ptr(q), ctypes.c_float(scale),
-                                    _ptr(out), _ptr(lse), ctypes.byref(ms) if timed else None), self.handle)
+        opts = kvc_attention_options(int(bool(accumulate)), float(decay))
+        _check(kvc_decode_attention_ex(self.handle, int(layer_begin), int(lc), _ptr(q), ctypes.c_float(scale),
+                                       ctypes.byref(opts), _ptr(out), _ptr(lse),
+                                       ctypes.byref(ms) if timed else None), self.handle)
         return (out, lse, ms.value) if timed else (out, lse)
 
     def check_wait_timeout(self, limit_ms: int = 100):
@@ -304,7 +350,7 @@ class Context:
         s = self.spec
         R, Ly, H, d = s.num_requests, s.num_layers, s.num_kv_heads, s.head_dim
         B, W, Hq = s.num_beacons, s.query_window, self.num_q_heads
-        es = self.k_pool.element_size()
+        es = 4 if self.dtype == torch.float32 else 2
         out = {
             "block_table": self._ws_tensor(v.block_table, R * v.max_pages_per_request * 4, torch.int32,
                                            (R, v.max_pages_per_request)),
@@ -326,12 +372,14 @@ class Context:
         return out
 
     def gather_dense(self, layer: int, req_begin: int = 0, req_count: int | None = None, cap: int | None = None):
-        """Dense copies (k, v [n, Hkv, cap, d], pos [n, Hkv, cap]) of one layer."""
+        """Dense copies (k, v [n, Hkv, cap, d], pos [n, Hkv, cap]) of one layer; k and v
+        of the 4-bit cache are float32, the values its codes stand for."""
         import torch
         s = self.spec
         n = s.num_requests - req_begin if req_count is None else req_count
         cap = s.max_seq_len if cap is None else cap
-        k = torch.empty((n, s.num_kv_heads, cap, s.head_dim), dtype=self.dtype, device=self.device)
+        k = torch.empty((n, s.num_kv_heads, cap, s.head_dim), dtype=torch.float32 if self.int4 else self.dtype,
+                        device=self.device)
         v = torch.empty_like(k)
         pos = torch.empty((n, s.num_kv_heads, cap), dtype=torch.int32, device=self.device)
         _check(kvc_gather_dense(self.handle, layer, req_begin, n, cap, _ptr(k), _ptr(v), _ptr(pos)),

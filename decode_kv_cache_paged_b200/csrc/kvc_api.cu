@@ -18,6 +18,7 @@
 #include <string>
 #include <vector>
 
+#include "int4.cuh"
 #include "kvc_internal.h"
 
 namespace {
@@ -49,7 +50,13 @@ struct Layout {
 // Split partials of the decode attention: room for this many splits of one layer.
 constexpr int kAttnSplits = 16;
 
-int elem_size(int dtype) { return dtype == KVC_BF16 ? 2 : 4; }
+// bytes of one element of the queries (and of K and V as they are appended)
+int elem_size(int dtype) { return dtype == KVC_F32 ? 4 : 2; }
+
+// bytes of one cached row
+int cache_row_bytes(const kvc_config &c) {
+  return c.dtype == KVC_INT4 ? int4_row_bytes(c.head_dim) : c.head_dim * elem_size(c.dtype);
+}
 
 // Returns an empty string if cfg is valid for this build, else the reason.
 std::string check_config(const kvc_config *c) {
@@ -59,7 +66,11 @@ std::string check_config(const kvc_config *c) {
   if (c->num_q_heads < c->num_kv_heads || c->num_q_heads % c->num_kv_heads != 0)
     return "num_q_heads must be a positive multiple of num_kv_heads";
   if (c->page_size != kPage) return "page_size must be 16";
-  if (c->dtype != KVC_BF16 && c->dtype != KVC_F32) return "dtype must be KVC_BF16 or KVC_F32";
+  if (c->dtype != KVC_BF16 && c->dtype != KVC_F32 && c->dtype != KVC_INT4)
+    return "dtype must be KVC_BF16, KVC_F32 or KVC_INT4";
+  if (c->dtype == KVC_INT4 && c->head_dim != 64 && c->head_dim != 128)
+    return "the 4-bit cache supports head_dim 64 or 128";
+  if (c->dtype == KVC_INT4 && c->num_beacons != 0) return "the 4-bit cache has no beacon selector (num_beacons must be 0)";
   const int rb = c->head_dim * elem_size(c->dtype);
   if (rb % 16 != 0 || rb > kMaxRowBytes)
     return "head_dim * sizeof(dtype) must be a multiple of 16 bytes and at most 1024";
@@ -139,7 +150,9 @@ struct kvc_ctx {
   int64_t round = 0;
   int score_impl = 0;
   int update_impl = 0;
-  int es = 2, row_bytes = 0, G = 1, maxp = 0, num_sms = 148;
+  int es = 2, row_bytes = 0, q_row_bytes = 0, G = 1, maxp = 0, num_sms = 148;
+  float *weights = nullptr;  // accumulated attention weights (caller's buffer), indexed like d_pos
+  int recent = 0;            // newest positions the attention selector always keeps
   float *d_attn = nullptr;
   std::string err;
 };
@@ -294,7 +307,8 @@ kvc_status kvc_create(const kvc_config *cfg, void *k_pool, void *v_pool, void *w
   c->v_pool = static_cast<uint8_t *>(v_pool);
   c->ws = static_cast<uint8_t *>(workspace);
   c->es = elem_size(cfg->dtype);
-  c->row_bytes = cfg->head_dim * c->es;
+  c->row_bytes = cache_row_bytes(*cfg);
+  c->q_row_bytes = cfg->head_dim * c->es;
   c->G = cfg->num_q_heads / cfg->num_kv_heads;
   c->maxp = cfg->max_seq_len / kPage;
   c->d_bt = reinterpret_cast<int32_t *>(c->ws + lay.bt);
@@ -393,6 +407,10 @@ kvc_status kvc_set_option(kvc_ctx *ctx, kvc_option opt, int64_t value) {
         return fail(ctx, KVC_ERR_UNSUPPORTED, "tcgen05 beacon update not available for this config");
       ctx->update_impl = (int)value;
       return KVC_OK;
+    case KVC_OPT_RECENT_TOKENS:
+      if (value < 0 || value > kMaxSeqLen) return fail(ctx, KVC_ERR_INVALID_ARG, "recent tokens must be in [0, 32768]");
+      ctx->recent = (int)value;
+      return KVC_OK;
   }
   return fail(ctx, KVC_ERR_INVALID_ARG, "unknown option");
 }
@@ -467,15 +485,18 @@ kvc_status kvc_append(kvc_ctx *ctx, const int32_t *req_ids, int32_t n_req, int32
   cudaError_t e;
   if ((e = launch_bt_scatter(reinterpret_cast<int32_t *>(st.d + (size_t)n_req * 32), n_pairs, ctx->d_bt, ctx->stream)) != cudaSuccess)
     return cuda_fail(ctx, e, "bt_scatter");
-  if ((e = launch_append_kv(static_cast<const uint8_t *>(k_new), static_cast<const uint8_t *>(v_new),
-                            ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->d_bt,
-                            reinterpret_cast<int32_t *>(st.d), n_req, c.num_layers, n_tokens,
-                            c.num_kv_heads, ctx->row_bytes, c.num_pages, ctx->maxp, ctx->stream)) != cudaSuccess)
-    return cuda_fail(ctx, e, "append_kv");
+  const int32_t *d_desc = reinterpret_cast<const int32_t *>(st.d);
+  const uint8_t *k_src = static_cast<const uint8_t *>(k_new), *v_src = static_cast<const uint8_t *>(v_new);
+  e = c.dtype == KVC_INT4
+          ? launch_append_kv4(k_src, v_src, ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->weights, ctx->d_bt, d_desc, n_req,
+                              c.num_layers, n_tokens, c.num_kv_heads, c.head_dim, c.num_pages, ctx->maxp, ctx->stream)
+          : launch_append_kv(k_src, v_src, ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->weights, ctx->d_bt, d_desc, n_req,
+                             c.num_layers, n_tokens, c.num_kv_heads, ctx->row_bytes, c.num_pages, ctx->maxp, ctx->stream);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "append_kv");
   if (q_new) {
     if ((e = launch_append_q(static_cast<const uint8_t *>(q_new), ctx->d_qring,
                              reinterpret_cast<int32_t *>(st.d + (size_t)n_req * 16), n_req,
-                             c.num_layers, n_tokens, t0, W, c.num_q_heads, ctx->row_bytes,
+                             c.num_layers, n_tokens, t0, W, c.num_q_heads, ctx->q_row_bytes,
                              ctx->stream)) != cudaSuccess)
       return cuda_fail(ctx, e, "append_q");
   }
@@ -574,14 +595,17 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
   if (!ctx) return KVC_ERR_INVALID_ARG;
   const kvc_config &c = ctx->cfg;
   if (selector != KVC_SEL_RANDOM && selector != KVC_SEL_RANDOM_SHARED && selector != KVC_SEL_BEACON &&
-      selector != KVC_SEL_BEACON_TRIGGER)
+      selector != KVC_SEL_BEACON_TRIGGER && selector != KVC_SEL_ATTENTION)
     return fail(ctx, KVC_ERR_INVALID_ARG, "unknown selector");
   if (!budgets) return fail(ctx, KVC_ERR_INVALID_ARG, "budgets is NULL");
   const kvc_round_options o = opts ? *opts : kvc_round_options{-1, 1, KVC_COMPACT_ORDERED, 0};
   if (o.block < 1 || o.block > kMaxSeqLen)
     return fail(ctx, KVC_ERR_INVALID_ARG, "block must be in [1, 32768]");
   const bool beacon_sel = selector == KVC_SEL_BEACON || selector == KVC_SEL_BEACON_TRIGGER;
-  if (o.block != 1 && beacon_sel)
+  const bool attn_sel = selector == KVC_SEL_ATTENTION;
+  if (attn_sel && !ctx->weights)
+    return fail(ctx, KVC_ERR_STATE, "the attention selector needs tracked weights (call kvc_bind_weights)");
+  if (o.block != 1 && (beacon_sel || attn_sel))
     return fail(ctx, KVC_ERR_INVALID_ARG, "block-granular draws apply to the random selectors only");
   if (o.compaction != KVC_COMPACT_ORDERED && o.compaction != KVC_COMPACT_HOLE_FILL)
     return fail(ctx, KVC_ERR_INVALID_ARG, "unknown compaction");
@@ -628,13 +652,21 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
   std::stable_sort(segs.begin(), segs.end(), [](const SegDesc &a, const SegDesc &b) {
     return (a.L - a.P) > (b.L - b.P);
   });
+  // attention selector: the newest `recent` positions of a request (no more
+  // than it keeps) always stay
+  std::vector<int32_t> recent_pos;
+  if (attn_sel)
+    for (const auto &s : segs)
+      recent_pos.push_back((int32_t)(ctx->h_next_pos[s.req] - std::min(ctx->recent, s.M)));
   const size_t seg_bytes = segs.size() * sizeof(SegDesc);
+  const size_t recent_off = align_up(seg_bytes, 16) + (size_t)R * 8;
   Stage sd_stage;
   if (kvc_status s = stage_acquire(ctx, sd_stage)) return s;
   std::memcpy(sd_stage.h, segs.data(), seg_bytes);
   std::memcpy(sd_stage.h + align_up(seg_bytes, 16), new_len.data(), (size_t)R * 4);
   std::memcpy(sd_stage.h + align_up(seg_bytes, 16) + (size_t)R * 4, new_prompt.data(), (size_t)R * 4);
-  if (kvc_status s = stage_upload(ctx, sd_stage, align_up(seg_bytes, 16) + (size_t)R * 8)) return s;
+  std::memcpy(sd_stage.h + recent_off, recent_pos.data(), recent_pos.size() * 4);
+  if (kvc_status s = stage_upload(ctx, sd_stage, recent_off + recent_pos.size() * 4)) return s;
   const SegDesc *d_segs = reinterpret_cast<const SegDesc *>(sd_stage.d);
   const bool timed = stats != nullptr;
   if (timed) {
@@ -680,6 +712,9 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
   sp.pos_map = ctx->d_pos;
   sp.block_table = ctx->d_bt;
   sp.scores = score_buf;
+  sp.weights = ctx->weights;
+  sp.recent = ctx->recent;
+  const int32_t *d_recent = reinterpret_cast<const int32_t *>(sd_stage.d + recent_off);
   sp.debug = (debug_scores && !beacon_sel) ? static_cast<uint32_t *>(debug_scores) : nullptr;
   sp.counters = ctx->d_counters;
   sp.status = ctx->d_status;
@@ -694,7 +729,8 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
   sp.seed = seed;
   sp.round = (uint64_t)ctx->round;
   const int mode = selector == KVC_SEL_RANDOM ? kModeRandom
-                   : selector == KVC_SEL_RANDOM_SHARED ? kModeRandomShared : kModeScores;
+                   : selector == KVC_SEL_RANDOM_SHARED ? kModeRandomShared
+                   : attn_sel ? kModeWeights : kModeScores;
   // launches: every segment with more than kSelectSmallMax candidates in one
   // (the kernel's persistent form, which balances the segments itself), the
   // others in buckets of candidate counts (2^(k-1), 2^k], k >= 10.  The split
@@ -718,6 +754,7 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
         ++i1;
       }
       sp.segs = d_segs + i0;
+      sp.recent_pos = attn_sel ? d_recent + i0 : nullptr;
       e = launch_select_compact(sp, mode, (int)(i1 - i0), max_n, max_m, ctx->stream);
       if (e != cudaSuccess) return cuda_fail(ctx, e, "select_compact");
       st.launches += 1;
@@ -804,16 +841,48 @@ kvc_status kvc_gather_dense(kvc_ctx *ctx, int32_t layer, int32_t req_begin, int3
     if (p && !device_ptr_on(ctx->device, p))
       return fail(ctx, KVC_ERR_INVALID_ARG, "outputs must be device memory");
   if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return fail(ctx, KVC_ERR_INVALID_ARG, "k_out/v_out must be 16-byte aligned");
-  cudaError_t e = launch_gather_dense(ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->d_bt, ctx->d_len, layer,
-                                      req_begin, req_count, cap, c.num_kv_heads, ctx->row_bytes,
-                                      c.num_pages, ctx->maxp, static_cast<uint8_t *>(k_out),
-                                      static_cast<uint8_t *>(v_out), pos_out, ctx->stream);
+  cudaError_t e =
+      c.dtype == KVC_INT4
+          ? launch_gather_dense4(ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->d_bt, ctx->d_len, layer, req_begin, req_count,
+                                 cap, c.num_kv_heads, c.head_dim, c.num_pages, ctx->maxp, static_cast<float *>(k_out),
+                                 static_cast<float *>(v_out), pos_out, ctx->stream)
+          : launch_gather_dense(ctx->k_pool, ctx->v_pool, ctx->d_pos, ctx->d_bt, ctx->d_len, layer, req_begin, req_count,
+                                cap, c.num_kv_heads, ctx->row_bytes, c.num_pages, ctx->maxp,
+                                static_cast<uint8_t *>(k_out), static_cast<uint8_t *>(v_out), pos_out, ctx->stream);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "gather_dense");
+  return KVC_OK;
+}
+
+kvc_status kvc_bind_weights(kvc_ctx *ctx, float *weights, size_t weights_bytes) {
+  NvtxRange nvtx_range("kvc_bind_weights");
+  if (!ctx) return KVC_ERR_INVALID_ARG;
+  const kvc_config &c = ctx->cfg;
+  if (!weights) {
+    ctx->weights = nullptr;
+    return KVC_OK;
+  }
+  if (c.head_dim != 64 && c.head_dim != 128)
+    return fail(ctx, KVC_ERR_UNSUPPORTED, "attention weights are tracked for head_dim 64 or 128");
+  const size_t need = (size_t)c.num_layers * (size_t)c.num_pages * c.num_kv_heads * kPage * 4;
+  if (weights_bytes < need)
+    return fail(ctx, KVC_ERR_INVALID_ARG, "weights too small: need " + std::to_string(need) + " bytes");
+  if ((uintptr_t)weights & 15) return fail(ctx, KVC_ERR_INVALID_ARG, "weights must be 16-byte aligned");
+  KVC_CUDA(ctx, cudaSetDevice(ctx->device));
+  if (!device_ptr_on(ctx->device, weights))
+    return fail(ctx, KVC_ERR_INVALID_ARG, "weights must be device memory of the context's device");
+  KVC_CUDA(ctx, cudaMemsetAsync(weights, 0, need, ctx->stream));
+  ctx->weights = weights;
   return KVC_OK;
 }
 
 kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,
                                 float scale, float *out, float *lse, float *ms_out) {
+  return kvc_decode_attention_ex(ctx, layer_begin, layer_count, q, scale, nullptr, out, lse, ms_out);
+}
+
+kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,
+                                   float scale, const kvc_attention_options *opts, float *out, float *lse,
+                                   float *ms_out) {
   NvtxRange nvtx_range("kvc_decode_attention");
   if (!ctx) return KVC_ERR_INVALID_ARG;
   const kvc_config &c = ctx->cfg;
@@ -821,6 +890,12 @@ kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer
     return fail(ctx, KVC_ERR_INVALID_ARG, "layer range out of bounds");
   if (!q || !out) return fail(ctx, KVC_ERR_INVALID_ARG, "q and out are required");
   if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(ctx, KVC_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  const kvc_attention_options o = opts ? *opts : kvc_attention_options{0, 1.f, {0, 0}};
+  if (o.accumulate != 0 && o.accumulate != 1) return fail(ctx, KVC_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  if (!(o.decay >= 0.f && o.decay <= 1.f)) return fail(ctx, KVC_ERR_INVALID_ARG, "decay must be in [0, 1]");
+  if (o.reserved[0] || o.reserved[1]) return fail(ctx, KVC_ERR_INVALID_ARG, "reserved option fields must be 0");
+  if (o.accumulate && !ctx->weights)
+    return fail(ctx, KVC_ERR_STATE, "accumulating needs tracked weights (call kvc_bind_weights)");
   KVC_CUDA(ctx, cudaSetDevice(ctx->device));
   if (!device_ptr_on(ctx->device, q) || !device_ptr_on(ctx->device, out) ||
       (lse && !device_ptr_on(ctx->device, lse)))
@@ -828,9 +903,10 @@ kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer
   if (((uintptr_t)q % ctx->es) || ((uintptr_t)out & 3) || ((uintptr_t)lse & 3))
     return fail(ctx, KVC_ERR_INVALID_ARG, "q, out or lse misaligned");
   const int G = ctx->G;
-  if (!decode_attention_supported(c.dtype, c.head_dim, G))
+  const bool plain = c.dtype != KVC_INT4 && !o.accumulate;  // the step without a 4-bit cache or weights
+  if (!(plain ? decode_attention_supported(c.dtype, c.head_dim, G) : decode_attention4_supported(c.dtype, c.head_dim, G)))
     return fail(ctx, KVC_ERR_UNSUPPORTED,
-                "decode attention needs bf16 or f32, head_dim 64 or 128 and 1, 2, 4 or 8 query heads per KV head");
+                "decode attention needs head_dim 64 or 128 and 1, 2, 4 or 8 query heads per KV head");
   const int R = c.num_requests;
   int max_len = 0;
   for (int r = 0; r < R; ++r) max_len = std::max(max_len, ctx->h_len[r]);
@@ -867,9 +943,12 @@ kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer
   p.nsplit = nsplit;
   p.pages_per_split = pps;
   p.qscale = (scale > 0.f ? scale : 1.0f / std::sqrt((float)c.head_dim)) * 1.4426950408889634f;
+  p.weights = o.accumulate ? ctx->weights : nullptr;
+  p.decay = o.decay;
   if (ms_out) KVC_CUDA(ctx, cudaEventRecord(ctx->ev[0], ctx->stream));
   int launches = 0;
-  cudaError_t e = launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream);
+  cudaError_t e = plain ? launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream)
+                        : launch_decode_attention4(p, c.head_dim, c.dtype, G, ctx->row_bytes, ctx->stream);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "decode_attention");
   if (ms_out) {
     KVC_CUDA(ctx, cudaEventRecord(ctx->ev[1], ctx->stream));

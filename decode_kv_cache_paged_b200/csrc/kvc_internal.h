@@ -22,7 +22,7 @@ constexpr int kDevIndex = 2;
 constexpr int kDevTimeout = 3;  // a bounded device wait ran out
 
 // Score sources of the fused select + compaction kernel.
-enum ScoreMode : int { kModeRandom = 0, kModeRandomShared = 1, kModeScores = 2 };
+enum ScoreMode : int { kModeRandom = 0, kModeRandomShared = 1, kModeScores = 2, kModeWeights = 3 };
 
 // One evicting request of a round: its pre-round length L, protected prompt
 // P and number M of generated positions to keep (0 < M < L - P).
@@ -36,6 +36,8 @@ struct SelectCompactParams {
   const int32_t *block_table;   // [R][bt_stride]
   const SegDesc *segs;          // [n_segs_req] one per request in this launch
   const float *scores;          // beacon scores [R][layers][Hkv][max_seq] (kModeScores)
+  float *weights;               // accumulated attention weights, indexed like pos_map; null = not tracked
+  const int32_t *recent_pos;    // [n_segs_req] positions from here on always stay (kModeWeights)
   uint32_t *debug;              // optional: candidate keys, same layout as scores
   unsigned long long *counters; // [0] moved rows
   int32_t *status;
@@ -43,6 +45,7 @@ struct SelectCompactParams {
   int32_t bt_stride, layers, hkv, row_bytes, max_seq;
   int32_t block;  // positions per Philox draw (random selectors)
   int32_t flags;  // kScTieByPos | kScHoleFill
+  int32_t recent; // at most this many positions are at or past recent_pos (kModeWeights)
   uint64_t seed, round;
 };
 
@@ -64,6 +67,8 @@ struct DecodeAttnParams {
   int64_t num_pages;
   int32_t bt_stride, layer_begin, layer_count, R, hkv, hq, nsplit, pages_per_split;
   float qscale;                // scale * log2(e)
+  float *weights;              // accumulated attention weights, indexed like the position map, or null
+  float decay;                 // weights <- decay * weights + this step's
 };
 
 // Beacon update over the query ring.
@@ -102,10 +107,18 @@ struct BeaconScoreParams {
 // Kernel launchers (each returns the launch error, if any).
 cudaError_t launch_bt_scatter(const int32_t *pairs, int n, int32_t *block_table, cudaStream_t s);
 cudaError_t launch_append_kv(const uint8_t *k_src, const uint8_t *v_src, uint8_t *k_pool,
-                             uint8_t *v_pool, int32_t *pos_map, const int32_t *block_table,
+                             uint8_t *v_pool, int32_t *pos_map, float *weights, const int32_t *block_table,
                              const int32_t *desc /* [n_req][4]: req, len_before, pos_before, - */,
                              int n_req, int layers, int T, int hkv, int row_bytes,
                              int64_t num_pages, int bt_stride, cudaStream_t s);
+cudaError_t launch_append_kv4(const uint8_t *k_src, const uint8_t *v_src, uint8_t *k_pool, uint8_t *v_pool,
+                              int32_t *pos_map, float *weights, const int32_t *block_table, const int32_t *desc,
+                              int n_req, int layers, int T, int hkv, int head_dim, int64_t num_pages,
+                              int bt_stride, cudaStream_t s);
+cudaError_t launch_gather_dense4(const uint8_t *k_pool, const uint8_t *v_pool, const int32_t *pos_map,
+                                 const int32_t *block_table, const int32_t *lengths, int layer, int req_begin,
+                                 int req_count, int cap, int hkv, int head_dim, int64_t num_pages, int bt_stride,
+                                 float *k_out, float *v_out, int32_t *pos_out, cudaStream_t s);
 cudaError_t launch_append_q(const uint8_t *q_src, uint8_t *qring,
                             const int32_t *desc /* [n_req][4]: req, ring slot of step 0, t0, - */,
                             int n_req, int layers, int T, int t0_global, int W, int hq,
@@ -119,6 +132,9 @@ cudaError_t launch_wait_timeout_probe(int32_t *status, uint32_t limit_ms, cudaSt
 bool decode_attention_supported(int dtype, int head_dim, int G);
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s);
+bool decode_attention4_supported(int dtype, int head_dim, int G);
+cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int dtype, int G, int row_bytes,
+                                     cudaStream_t s);
 cudaError_t launch_select_compact(const SelectCompactParams &p, int mode, int n_seg_req,
                                   int max_n, int max_m, cudaStream_t s);
 cudaError_t launch_beacon_update(const BeaconUpdateParams &p, int n_req, cudaStream_t s);

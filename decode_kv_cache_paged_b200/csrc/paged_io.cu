@@ -7,11 +7,17 @@
 // last W steps for the periodic beacon update.
 // gather_dense: a dense copy of one layer, used to check the cache against
 // the oracle.
+// The 4-bit cache (KVC_INT4) has an append that codes the rows on their way
+// into the pool and a gather that returns the values the codes stand for.
+// Where the context tracks attention weights, an appended row starts at 0.
 //
-// All three kernels move 16-byte vectors, one per thread, with consecutive
+// All kernels but the 4-bit ones move 16-byte vectors, one per thread, with consecutive
 // threads on consecutive bytes of the source (coalesced reads; writes are
 // contiguous per row).  Sources may be page-locked host memory, read over
 // PCIe through the unified address space.
+#include <math_constants.h>
+
+#include "int4.cuh"
 #include "kvc_internal.h"
 
 namespace kvc {
@@ -26,7 +32,8 @@ __global__ void bt_scatter_kernel(const int32_t *__restrict__ pairs, int n,
 // source [n_req][layers][T][hkv][row] ; one thread per 16-byte vector
 __global__ void append_kv_kernel(const uint8_t *__restrict__ k_src, const uint8_t *__restrict__ v_src,
                                  uint8_t *__restrict__ k_pool, uint8_t *__restrict__ v_pool,
-                                 int32_t *__restrict__ pos_map, const int32_t *__restrict__ block_table,
+                                 int32_t *__restrict__ pos_map, float *__restrict__ weights,
+                                 const int32_t *__restrict__ block_table,
                                  const int4 *__restrict__ desc, int layers, int T, int hkv,
                                  int vpr, int64_t total, int64_t num_pages, int bt_stride) {
   const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -47,7 +54,84 @@ __global__ void append_kv_kernel(const uint8_t *__restrict__ k_src, const uint8_
   const int64_t dst = row * vpr * 16 + (int64_t)v * 16;
   *reinterpret_cast<uint4 *>(k_pool + dst) = *reinterpret_cast<const uint4 *>(k_src + g * 16);
   *reinterpret_cast<uint4 *>(v_pool + dst) = *reinterpret_cast<const uint4 *>(v_src + g * 16);
-  if (v == 0) pos_map[row] = d.z + t;
+  if (v == 0) {
+    pos_map[row] = d.z + t;
+    if (weights) weights[row] = 0.f;
+  }
+}
+
+// 4-bit append.  D/8 neighbouring lanes take one row, 8 channels (16 bytes of
+// bf16) each, so a group of D/4 channels is 4 lanes (D = 128) or 2 (D = 64):
+// its smallest and largest value come from one or two shuffles, and the lanes
+// of a row write its codes 4 bytes apiece, side by side.
+template <int D>
+__device__ __forceinline__ void int4_code_chunk(uint4 x4, uint8_t *row, int v, unsigned lanes) {
+  constexpr int kLanes = D / 8 / kInt4Groups;  // lanes of one group
+  const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  float lo = x[0], hi = x[0], bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+    bad = fmaf(x[i], 0.f, bad);  // NaN once a value is infinite or NaN
+  }
+#pragma unroll
+  for (int m = 1; m < kLanes; m <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(lanes, lo, m));
+    hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, m));
+    bad += __shfl_xor_sync(lanes, bad, m);
+  }
+  float s = int4_step(lo, hi) + bad;
+  if (isnan(s)) lo = s;
+  uint32_t codes = 0;
+  if (s > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) codes |= (uint32_t)__float2int_rn(__fdiv_rn(x[i] - lo, s)) << (4 * i);
+  }
+  if (v % kLanes == 0) {
+    const uint32_t h = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+    *reinterpret_cast<uint32_t *>(row + (v / kLanes) * 4) = h;
+  }
+  *reinterpret_cast<uint32_t *>(row + kInt4Header + v * 4) = codes;
+}
+
+template <int D>
+__global__ void append_kv4_kernel(const uint4 *__restrict__ k_src, const uint4 *__restrict__ v_src,
+                                  uint8_t *__restrict__ k_pool, uint8_t *__restrict__ v_pool,
+                                  int32_t *__restrict__ pos_map, float *__restrict__ weights,
+                                  const int32_t *__restrict__ block_table, const int4 *__restrict__ desc,
+                                  int layers, int T, int hkv, int64_t total, int64_t num_pages, int bt_stride) {
+  constexpr int vpr = D / 8;
+  const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  // total is a multiple of vpr, so the lanes of a row leave together
+  const unsigned lanes = __ballot_sync(0xffffffffu, g < total);
+  if (g >= total) return;
+  int64_t rest = g;
+  const int v = (int)(rest % vpr);
+  rest /= vpr;
+  const int h = (int)(rest % hkv);
+  rest /= hkv;
+  const int t = (int)(rest % T);
+  rest /= T;
+  const int l = (int)(rest % layers);
+  const int i = (int)(rest / layers);
+  const int4 d = desc[i];  // req, len_before, pos_before
+  const int slot = d.y + t;
+  const int page = block_table[(int64_t)d.x * bt_stride + (slot >> 4)];
+  const int64_t row = (((int64_t)l * num_pages + page) * hkv + h) * kPage + (slot & (kPage - 1));
+  const uint4 kx = k_src[g], vx = v_src[g];
+  int4_code_chunk<D>(kx, k_pool + row * int4_row_bytes(D), v, lanes);
+  int4_code_chunk<D>(vx, v_pool + row * int4_row_bytes(D), v, lanes);
+  if (v == 0) {
+    pos_map[row] = d.z + t;
+    if (weights) weights[row] = 0.f;
+  }
 }
 
 // source [n_req][layers][T][hq][row]; only the last W steps are written
@@ -104,6 +188,59 @@ __global__ void gather_dense_kernel(const uint8_t *__restrict__ k_pool, const ui
   if (pos_out && v == 0) pos_out[g / vpr] = pos;
 }
 
+// the values of 8 codes of group (v * 8) / (D / 4): one lane's share of a row
+template <int D>
+__device__ __forceinline__ void int4_values(const uint8_t *row, int v, float4 &a, float4 &b) {
+  const uint32_t h = *reinterpret_cast<const uint32_t *>(row + (v * 8 / (D / kInt4Groups)) * 4);
+  const uint32_t c = *reinterpret_cast<const uint32_t *>(row + kInt4Header + v * 4);
+  const float s = __uint_as_float(h << 16), lo = __uint_as_float(h & 0xffff0000u);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((c >> (4 * i)) & 15u), s, lo);
+  a = make_float4(x[0], x[1], x[2], x[3]);
+  b = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// dense fp32 copy of one layer of the 4-bit cache
+template <int D>
+__global__ void gather_dense4_kernel(const uint8_t *__restrict__ k_pool, const uint8_t *__restrict__ v_pool,
+                                     const int32_t *__restrict__ pos_map, const int32_t *__restrict__ block_table,
+                                     const int32_t *__restrict__ lengths, int layer, int req_begin, int cap,
+                                     int hkv, int64_t total, int64_t num_pages, int bt_stride,
+                                     float4 *__restrict__ k_out, float4 *__restrict__ v_out,
+                                     int32_t *__restrict__ pos_out) {
+  constexpr int vpr = D / 8;
+  const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (g >= total) return;
+  int64_t rest = g;
+  const int v = (int)(rest % vpr);
+  rest /= vpr;
+  const int slot = (int)(rest % cap);
+  rest /= cap;
+  const int h = (int)(rest % hkv);
+  const int i = (int)(rest / hkv);
+  const int r = req_begin + i;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 k0 = zero, k1 = zero, v0 = zero, v1 = zero;
+  int pos = -1;
+  if (slot < lengths[r]) {
+    const int page = block_table[(int64_t)r * bt_stride + (slot >> 4)];
+    const int64_t row = (((int64_t)layer * num_pages + page) * hkv + h) * kPage + (slot & (kPage - 1));
+    if (k_out) int4_values<D>(k_pool + row * int4_row_bytes(D), v, k0, k1);
+    if (v_out) int4_values<D>(v_pool + row * int4_row_bytes(D), v, v0, v1);
+    pos = pos_map[row];
+  }
+  if (k_out) {
+    k_out[2 * g] = k0;
+    k_out[2 * g + 1] = k1;
+  }
+  if (v_out) {
+    v_out[2 * g] = v0;
+    v_out[2 * g + 1] = v1;
+  }
+  if (pos_out && v == 0) pos_out[g / vpr] = pos;
+}
+
 inline unsigned blocks_for(int64_t total, int nt) { return (unsigned)((total + nt - 1) / nt); }
 
 }  // namespace
@@ -115,15 +252,28 @@ cudaError_t launch_bt_scatter(const int32_t *pairs, int n, int32_t *block_table,
 }
 
 cudaError_t launch_append_kv(const uint8_t *k_src, const uint8_t *v_src, uint8_t *k_pool,
-                             uint8_t *v_pool, int32_t *pos_map, const int32_t *block_table,
-                             const int32_t *desc, int n_req, int layers, int T, int hkv,
-                             int row_bytes, int64_t num_pages, int bt_stride, cudaStream_t s) {
+                             uint8_t *v_pool, int32_t *pos_map, float *weights,
+                             const int32_t *block_table, const int32_t *desc, int n_req, int layers, int T,
+                             int hkv, int row_bytes, int64_t num_pages, int bt_stride, cudaStream_t s) {
   const int vpr = row_bytes / 16;
   const int64_t total = (int64_t)n_req * layers * T * hkv * vpr;
   if (total <= 0) return cudaSuccess;
   append_kv_kernel<<<blocks_for(total, 256), 256, 0, s>>>(
-      k_src, v_src, k_pool, v_pool, pos_map, block_table, reinterpret_cast<const int4 *>(desc),
+      k_src, v_src, k_pool, v_pool, pos_map, weights, block_table, reinterpret_cast<const int4 *>(desc),
       layers, T, hkv, vpr, total, num_pages, bt_stride);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append_kv4(const uint8_t *k_src, const uint8_t *v_src, uint8_t *k_pool, uint8_t *v_pool,
+                              int32_t *pos_map, float *weights, const int32_t *block_table, const int32_t *desc,
+                              int n_req, int layers, int T, int hkv, int head_dim, int64_t num_pages,
+                              int bt_stride, cudaStream_t s) {
+  const int64_t total = (int64_t)n_req * layers * T * hkv * (head_dim / 8);
+  if (total <= 0) return cudaSuccess;
+  auto kernel = head_dim == 128 ? append_kv4_kernel<128> : append_kv4_kernel<64>;
+  kernel<<<blocks_for(total, 256), 256, 0, s>>>(
+      reinterpret_cast<const uint4 *>(k_src), reinterpret_cast<const uint4 *>(v_src), k_pool, v_pool, pos_map,
+      weights, block_table, reinterpret_cast<const int4 *>(desc), layers, T, hkv, total, num_pages, bt_stride);
   return cudaGetLastError();
 }
 
@@ -149,6 +299,19 @@ cudaError_t launch_gather_dense(const uint8_t *k_pool, const uint8_t *v_pool,
   gather_dense_kernel<<<blocks_for(total, 256), 256, 0, s>>>(
       k_pool, v_pool, pos_map, block_table, lengths, layer, req_begin, cap, hkv, vpr, total,
       num_pages, bt_stride, k_out, v_out, pos_out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_dense4(const uint8_t *k_pool, const uint8_t *v_pool, const int32_t *pos_map,
+                                 const int32_t *block_table, const int32_t *lengths, int layer, int req_begin,
+                                 int req_count, int cap, int hkv, int head_dim, int64_t num_pages, int bt_stride,
+                                 float *k_out, float *v_out, int32_t *pos_out, cudaStream_t s) {
+  const int64_t total = (int64_t)req_count * hkv * cap * (head_dim / 8);
+  if (total <= 0) return cudaSuccess;
+  auto kernel = head_dim == 128 ? gather_dense4_kernel<128> : gather_dense4_kernel<64>;
+  kernel<<<blocks_for(total, 256), 256, 0, s>>>(
+      k_pool, v_pool, pos_map, block_table, lengths, layer, req_begin, cap, hkv, total, num_pages, bt_stride,
+      reinterpret_cast<float4 *>(k_out), reinterpret_cast<float4 *>(v_out), pos_out);
   return cudaGetLastError();
 }
 

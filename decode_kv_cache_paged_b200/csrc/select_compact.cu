@@ -6,7 +6,8 @@
 // 只随机保留" and "发现四"): the protected slots [0, P) are never candidates;
 // the N = L - P candidate slots are ranked by (score desc, original position
 // asc), the best M stay and are compacted into slots [P, P + M); K rows, V
-// rows and the position map move together.  The score is the Philox draw of
+// rows, the position map and any tracked attention weights move together.
+// The score is the Philox draw of
 // the (position / block, head, layer, request) counter for the random
 // selectors (block = 1: one draw per position; larger blocks keep contiguous
 // runs, "发现二"), or the precomputed beacon score.
@@ -14,7 +15,8 @@
 // Design (B200): one CTA per segment, everything between score and copy in
 // shared memory.
 //   1. score: each thread draws the 32-bit keys of a strided set of slots
-//      (the random path reads only the 4-byte position map, never K/V);
+//      (the random path reads only the 4-byte position map, the attention
+//      path only the 4-byte accumulated weights, never K/V);
 //   2. select: 4-pass MSB radix select (8-bit digits, shared-memory
 //      histogram) finds the M-th largest key tau, how many keys equal tau and
 //      how many of those stay.  When slots are in position order (always, as
@@ -224,6 +226,7 @@ struct ScSeg {
   int h, l, r, P, M, N;
   const int32_t *bt;
   int64_t layer_page0, seg_flat;
+  int recent_pos;  // attention selector: positions from here on stay
 };
 
 __device__ __forceinline__ ScSeg sc_seg(const SelectCompactParams &p, int item) {
@@ -238,6 +241,7 @@ __device__ __forceinline__ ScSeg sc_seg(const SelectCompactParams &p, int item) 
   g.bt = p.block_table + (int64_t)g.r * p.bt_stride;
   g.layer_page0 = (int64_t)g.l * p.num_pages;
   g.seg_flat = ((int64_t)g.r * p.layers + g.l) * p.hkv + g.h;
+  g.recent_pos = p.recent_pos ? p.recent_pos[item / (p.hkv * p.layers)] : 0x7fffffff;
   return g;
 }
 
@@ -246,12 +250,36 @@ __device__ __forceinline__ int64_t sc_row(const SelectCompactParams &p, const Sc
   return ((g.layer_page0 + g.bt[s >> 4]) * p.hkv + g.h) * kPage + (s & (kPage - 1));
 }
 
+// Ranking key of candidate j from its accumulated attention weight: the
+// largest key for a position that always stays (the newest ones; at most as
+// many as are kept), else the weight's order key.  A NaN weight is reported
+// and ranks below every other one.  Positions increase with the slot unless a
+// round filled holes (kScTieByPos), so only the last `recent` candidates can
+// be that new and the others' positions need not be read.
+__device__ __forceinline__ uint32_t sc_weight_key(const SelectCompactParams &p, const ScSeg &g, int j, float w) {
+  if (p.debug) p.debug[g.seg_flat * p.max_seq + j] = __float_as_uint(w);
+  if (((p.flags & kScTieByPos) || j >= g.N - p.recent) && p.pos_map[sc_row(p, g, g.P + j)] >= g.recent_pos)
+    return 0xffffffffu;
+  if (isnan(w)) {
+    atomicCAS(p.status, kDevOk, kDevNaN);
+    return 0u;
+  }
+  return float_order_key(w);
+}
+
+// The 4-byte word that moves with each row beside its K and V: a row's first
+// thread carries its position, the second its attention weight (null: none).
+__device__ __forceinline__ int32_t *sc_side(const SelectCompactParams &p, int my_vec) {
+  return my_vec == 0 ? p.pos_map : my_vec == 1 ? reinterpret_cast<int32_t *>(p.weights) : nullptr;
+}
+
 // 32-bit ranking key of candidate j (slot P + j): the order key of the beacon
-// score, or the high word of the Philox draw of (position / block, head,
-// layer, request) under (seed, round)
+// score or of the accumulated attention weight, or the high word of the
+// Philox draw of (position / block, head, layer, request) under (seed, round)
 template <int MODE>
 __device__ __forceinline__ uint32_t sc_key(const SelectCompactParams &p, const ScSeg &g, int j) {
   if (MODE == kModeScores) return float_order_key(p.scores[g.seg_flat * p.max_seq + j]);
+  if (MODE == kModeWeights) return sc_weight_key(p, g, j, p.weights[sc_row(p, g, g.P + j)]);
   const uint64_t head_field = (MODE == kModeRandomShared) ? ~0ull : (uint64_t)g.h;
   const int pos = p.pos_map[sc_row(p, g, g.P + j)];
   const uint32_t key = philox4x64_10_word0_hi32((uint64_t)(int64_t)(pos / p.block), head_field, (uint64_t)g.l,
@@ -406,6 +434,7 @@ __global__ void __launch_bounds__(NT) select_compact_kernel(SelectCompactParams 
   const int my_row = tid / vpr, my_vec = tid - (tid / vpr) * vpr;
   const bool active = my_row < rows_per_pass;
   const int64_t rb = p.row_bytes;
+  int32_t *const side = sc_side(p, my_vec);
 
   if (VAR != kHoleFill) {
     // 3. ranks in slot order
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(NT) select_compact_kernel(SelectCompactParams 
           drow[u] = sc_row(p, g, P + q);
           kr[u] = *reinterpret_cast<const uint4 *>(p.k_pool + srow * rb + my_vec * 16);
           vr[u] = *reinterpret_cast<const uint4 *>(p.v_pool + srow * rb + my_vec * 16);
-          if (my_vec == 0) pr[u] = p.pos_map[srow];
+          if (side) pr[u] = side[srow];
         }
       }
       __syncthreads();
@@ -436,7 +465,7 @@ __global__ void __launch_bounds__(NT) select_compact_kernel(SelectCompactParams 
         if (drow[u] >= 0) {
           *reinterpret_cast<uint4 *>(p.k_pool + drow[u] * rb + my_vec * 16) = kr[u];
           *reinterpret_cast<uint4 *>(p.v_pool + drow[u] * rb + my_vec * 16) = vr[u];
-          if (my_vec == 0) p.pos_map[drow[u]] = pr[u];
+          if (side) side[drow[u]] = pr[u];
         }
       }
     }
@@ -467,7 +496,7 @@ __global__ void __launch_bounds__(NT) select_compact_kernel(SelectCompactParams 
           drow[u] = sc_row(p, g, P + src_of_rank[i]);
           kr[u] = *reinterpret_cast<const uint4 *>(p.k_pool + srow * rb + my_vec * 16);
           vr[u] = *reinterpret_cast<const uint4 *>(p.v_pool + srow * rb + my_vec * 16);
-          if (my_vec == 0) pr[u] = p.pos_map[srow];
+          if (side) pr[u] = side[srow];
         }
       }
 #pragma unroll
@@ -475,7 +504,7 @@ __global__ void __launch_bounds__(NT) select_compact_kernel(SelectCompactParams 
         if (drow[u] >= 0) {
           *reinterpret_cast<uint4 *>(p.k_pool + drow[u] * rb + my_vec * 16) = kr[u];
           *reinterpret_cast<uint4 *>(p.v_pool + drow[u] * rb + my_vec * 16) = vr[u];
-          if (my_vec == 0) p.pos_map[drow[u]] = pr[u];
+          if (side) side[drow[u]] = pr[u];
         }
       }
     }
@@ -493,11 +522,13 @@ __device__ __forceinline__ void cp_async4(void *smem_dst, const void *gsrc) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The key of candidate j from the raw word fetched for it: the score's bits
-// (kModeScores) or its position (random selectors).
+// The key of candidate j from the raw word fetched for it: the score's or the
+// weight's bits (kModeScores, kModeWeights) or its position (random
+// selectors).
 template <int MODE>
 __device__ __forceinline__ uint32_t sc_key_from(const SelectCompactParams &p, const ScSeg &g, int j, uint32_t raw) {
   if (MODE == kModeScores) return float_order_key(__uint_as_float(raw));
+  if (MODE == kModeWeights) return sc_weight_key(p, g, j, __uint_as_float(raw));
   const uint64_t head_field = (MODE == kModeRandomShared) ? ~0ull : (uint64_t)g.h;
   const uint32_t key = philox4x64_10_word0_hi32((uint64_t)(int64_t)((int)raw / p.block), head_field, (uint64_t)g.l,
                                                 (uint64_t)g.r, p.seed, p.round);
@@ -522,7 +553,8 @@ __host__ __device__ __forceinline__ int *sc_work_counter(const SelectCompactPara
 //   - before chunk 0, cp.async brings the next segment's block-table row
 //     (and, for beacon scores, the scores themselves) into shared memory;
 //   - after chunk 0's barrier has made that row visible, cp.async brings the
-//     position of every candidate (random selectors) into the keys buffer;
+//     position (random selectors) or the accumulated weight (attention
+//     selector) of every candidate into the keys buffer;
 //   - from the next chunk on, between issuing the chunk's loads and its
 //     barrier, each thread turns a share of the words it fetched itself into
 //     keys (Philox draws, or the scores' order keys) and counts their top
@@ -572,6 +604,7 @@ __global__ void __launch_bounds__(512, 1)
   const int my_row = tid / vpr, my_vec = tid - (tid / vpr) * vpr;
   const bool active = my_row < rows_per_pass;
   const int64_t rb = p.row_bytes;
+  int32_t *const side = sc_side(p, my_vec);
 
 #pragma unroll 1
   while (true) {
@@ -603,10 +636,11 @@ __global__ void __launch_bounds__(512, 1)
       cp_async_commit();
       gn.bt = bt_next;  // read only once chunk 0's barrier (or the tail's) has made it visible
     }
-    // positions of the next segment's candidates (random selectors)
+    // positions (random selectors) or weights of the next segment's candidates
     auto fetch_positions = [&]() {
       if (MODE != kModeScores) {
-        for (int j = tid; j < nn; j += NT) cp_async4(keys + j, p.pos_map + sc_row(p, gn, gn.P + j));
+        const int32_t *src = MODE == kModeWeights ? reinterpret_cast<const int32_t *>(p.weights) : p.pos_map;
+        for (int j = tid; j < nn; j += NT) cp_async4(keys + j, src + sc_row(p, gn, gn.P + j));
         cp_async_commit();
       }
     };
@@ -625,7 +659,7 @@ __global__ void __launch_bounds__(512, 1)
           const int64_t srow = sc_row(p, g, P + src_of_rank[q]);
           kr[u] = *reinterpret_cast<const uint4 *>(p.k_pool + srow * rb + my_vec * 16);
           vr[u] = *reinterpret_cast<const uint4 *>(p.v_pool + srow * rb + my_vec * 16);
-          if (my_vec == 0) pr[u] = p.pos_map[srow];
+          if (side) pr[u] = side[srow];
         }
       }
       if (c == 0) {
@@ -650,7 +684,7 @@ __global__ void __launch_bounds__(512, 1)
           const int64_t drow = sc_row(p, g, P + q);
           *reinterpret_cast<uint4 *>(p.k_pool + drow * rb + my_vec * 16) = kr[u];
           *reinterpret_cast<uint4 *>(p.v_pool + drow * rb + my_vec * 16) = vr[u];
-          if (my_vec == 0) p.pos_map[drow] = pr[u];
+          if (side) side[drow] = pr[u];
         }
       }
     }
@@ -748,6 +782,7 @@ cudaError_t launch_nt(const SelectCompactParams &p, int mode, int var, int n_seg
     case kModeRandom: return launch_var<NT, U, kModeRandom>(p, var, n_seg_req, keys_cap, m_cap, smem, s);
     case kModeRandomShared:
       return launch_var<NT, U, kModeRandomShared>(p, var, n_seg_req, keys_cap, m_cap, smem, s);
+    case kModeWeights: return launch_var<NT, U, kModeWeights>(p, var, n_seg_req, keys_cap, m_cap, smem, s);
     default: return launch_var<NT, U, kModeScores>(p, var, n_seg_req, keys_cap, m_cap, smem, s);
   }
 }

@@ -4,8 +4,9 @@
  *
  * The round, for every segment s = (request r, layer l, KV head h):
  *   (a) scores the generated positions with the Random-Attention selector (a
- *       counter-based Philox score per head and position) or with the BeaconKV
- *       selector (maximum softmax mass over the segment's beacons);
+ *       counter-based Philox score per head and position), with the BeaconKV
+ *       selector (maximum softmax mass over the segment's beacons) or by the
+ *       attention weight that decode attention has accumulated on each row;
  *   (b) never evicts the protected prompt;
  *   (c) keeps the top positions by (score desc, original position asc)
  *       against the request's budget K;
@@ -82,20 +83,37 @@ typedef enum {
   KVC_ERR_UNSUPPORTED = 8     /* valid request this build does not support */
 } kvc_status;
 
-typedef enum { KVC_BF16 = 0, KVC_F32 = 1 } kvc_dtype;
+/* KVC_INT4 is a 4-bit cache: K, V and queries are given in bf16 and a cached
+ * row of head_dim channels (64 or 128) is kept as four groups of head_dim/4
+ * channels.  With lo and hi a group's smallest and largest value,
+ *     s     = (hi - lo) / 15 rounded up to four significant bits
+ *             (0 where (hi - lo) / 15 < 2^-100),
+ *     code  = rint((x - lo) / s), ties to even (0 where s = 0),
+ *     value = lo + s * code,
+ * so a value is off by at most s / 2; a group that holds an infinity or a
+ * NaN, or whose (hi - lo) / 15 reaches 2^100, stands for NaN.  Row bytes: the
+ * (s, lo) bf16 pairs of groups 0..3, then head_dim/2 bytes of codes, the
+ * lower channel in a byte's low half: head_dim/2 + 16 in all (80 at head_dim
+ * 128, against 256 in bf16).  The random and the attention selectors, both
+ * compactions and decode attention work on it; the beacon selectors do not
+ * (num_beacons must be 0). */
+typedef enum { KVC_BF16 = 0, KVC_F32 = 1, KVC_INT4 = 2 } kvc_dtype;
 
 typedef enum {
   KVC_SEL_RANDOM = 0,        /* [RA]: independent Philox score per head and position */
   KVC_SEL_RANDOM_SHARED = 1, /* [RA "发现二"]: one score per (request, layer, position) */
   KVC_SEL_BEACON = 2,        /* [BX]/[BA]: max over beacons of softmax(c.K^T/sqrt(d)) */
-  KVC_SEL_BEACON_TRIGGER = 3 /* [BX] §3.2 cluster-level trigger: sum over beacons of the latest
+  KVC_SEL_BEACON_TRIGGER = 3, /* [BX] §3.2 cluster-level trigger: sum over beacons of the latest
                                 update's share of points in the beacon's cluster times the
                                 beacon's softmax (see kvc_compress) */
+  KVC_SEL_ATTENTION = 4      /* the attention weight each row has gathered over the decode steps
+                                (kvc_bind_weights, kvc_decode_attention_ex), beside the newest
+                                KVC_OPT_RECENT_TOKENS positions */
 } kvc_selector;
 
 /* Limits of this build (checked by kvc_create):
  *   page_size == 16; head_dim * sizeof(dtype) a multiple of 16 bytes and
- *   <= 1024 bytes; max_seq_len a multiple of 16 and <= 32768;
+ *   <= 1024 bytes (KVC_INT4: head_dim 64 or 128, num_beacons 0); max_seq_len a multiple of 16 and <= 32768;
  *   num_beacons in [0, 256]; query_window * (num_q_heads / num_kv_heads)
  *   <= 4096; num_q_heads a multiple of num_kv_heads. */
 typedef struct {
@@ -148,15 +166,19 @@ typedef struct {
   float *beacon_triggers;     /* [num_requests][num_layers][num_kv_heads][B]: share of the latest
                                  update's points assigned to each beacon */
   int32_t max_pages_per_request;
-  int32_t row_bytes;          /* head_dim * sizeof(dtype) */
+  int32_t row_bytes;          /* bytes of a cached row: head_dim * sizeof(dtype), KVC_INT4
+                                 head_dim/2 + 16 */
   int64_t round;              /* rounds completed */
 } kvc_view;
 
 typedef enum {
   KVC_OPT_BEACON_SCORE_IMPL = 0, /* 0 auto, 1 SIMT fp32 kernel, 2 tcgen05 (bf16, head_dim 128) */
-  KVC_OPT_BEACON_UPDATE_IMPL = 1 /* 0 auto, 1 SIMT fp32 kernel, 2 tcgen05 assignment (bf16, head_dim 128,
+  KVC_OPT_BEACON_UPDATE_IMPL = 1, /* 0 auto, 1 SIMT fp32 kernel, 2 tcgen05 assignment (bf16, head_dim 128,
                                     B a multiple of 32): x.c as x.c_hi + x.c_lo with bf16 terms of the
                                     fp32 beacons, error <= 2^-18 sum_k |x_k c_k| beyond fp32 rounding */
+  KVC_OPT_RECENT_TOKENS = 2       /* newest positions that KVC_SEL_ATTENTION always keeps, 0 (the
+                                    default) to 32768: of the M rows that a round keeps of a
+                                    request beside its prompt, the newest min(value, M) */
 } kvc_option;
 
 typedef struct kvc_ctx kvc_ctx;
@@ -169,7 +191,8 @@ size_t kvc_workspace_bytes(const kvc_config *cfg);
 
 /* Creates a context over caller-allocated device memory.
  *   k_pool, v_pool: device, 256-byte aligned, each
- *     num_layers*num_pages*num_kv_heads*16*head_dim*sizeof(dtype) bytes.
+ *     num_layers*num_pages*num_kv_heads*16*head_dim*sizeof(dtype) bytes
+ *     (KVC_INT4: head_dim/2 + 16 bytes for each row instead).
  *   workspace: device, 256-byte aligned, >= kvc_workspace_bytes(cfg) bytes;
  *     its contents are initialised here (enqueued on the stream).
  *   cuda_stream: cudaStream_t on the pools' device (NULL = legacy stream).
@@ -187,7 +210,8 @@ kvc_status kvc_set_option(kvc_ctx *ctx, kvc_option opt, int64_t value);
 
 /* Appends n_tokens decode (or prompt) tokens to each listed request.
  *   req_ids: host int32[n_req], distinct, in [0, num_requests).
- *   k_new, v_new: [n_req][num_layers][n_tokens][num_kv_heads][head_dim] dtype,
+ *   k_new, v_new: [n_req][num_layers][n_tokens][num_kv_heads][head_dim] dtype
+ *     (bf16 for KVC_INT4, which codes the rows on their way into the cache),
  *     device memory or page-locked host memory (read over PCIe by the kernel).
  *   q_new: [n_req][num_layers][n_tokens][num_q_heads][head_dim] dtype, same
  *     memory rules, or NULL.  The queries of the last query_window steps are
@@ -196,6 +220,7 @@ kvc_status kvc_set_option(kvc_ctx *ctx, kvc_option opt, int64_t value);
  *   protect: 1 = the tokens belong to the protected prompt [RA]; only valid
  *     while the request holds no generated token (else KVC_ERR_STATE).
  * Token t of request i takes position (its length before the call) + t.
+ * Where weights are tracked (kvc_bind_weights) the new rows start at 0.
  * Errors (nothing enqueued): KVC_ERR_INVALID_ARG, KVC_ERR_STATE,
  * KVC_ERR_OUT_OF_PAGES (max_seq_len or the pool would overflow). */
 kvc_status kvc_append(kvc_ctx *ctx, const int32_t *req_ids, int32_t n_req, int32_t n_tokens,
@@ -233,9 +258,15 @@ kvc_status kvc_update_beacons(kvc_ctx *ctx, int32_t *assign_out, float *ms_out);
  *   [BX] §3.2 mark_important, read as: each query of the latest update raises
  *   the keys its cluster's beacon attends to) = sum_b w_b exp(z_bj - lse_b)
  *   with w_b the share of the latest update's points assigned to beacon b.
+ *   Attention score (KVC_SEL_ATTENTION; needs kvc_bind_weights, else
+ *   KVC_ERR_STATE) = the row's accumulated weight; the request's newest
+ *   min(KVC_OPT_RECENT_TOKENS, M) positions, with M = max(0, K-P), stay
+ *   whatever their weight.  A NaN weight ranks below every other one and is
+ *   reported as KVC_ERR_NAN by the next synchronising call.  Tracked weights
+ *   move with their rows, whatever the selector.
  *   debug_scores: device, NULL or [R][num_layers][num_kv_heads][max_seq_len]
  *     32-bit; receives each candidate's score at index j - P (uint32 for the
- *     random selectors, float for the beacon selector).
+ *     random selectors, float for the beacon and attention selectors).
  *   stats: host, NULL or filled after synchronising the stream.
  * The round counter advances by one on success. */
 kvc_status kvc_compress(kvc_ctx *ctx, kvc_selector selector, const int32_t *budgets,
@@ -249,7 +280,7 @@ kvc_status kvc_compress(kvc_ctx *ctx, kvc_selector selector, const int32_t *budg
  *     regimes); the rest of the prompt competes with the generated
  *     positions, and the request's protected length becomes min(P, S) for
  *     later rounds once a round evicts from it.
- *   block: random selectors only (must be 1 for the beacon selector),
+ *   block: random selectors only (must be 1 for the other selectors),
  *     1 <= block <= 32768: the positions of one block, pos / block, share one
  *     Philox draw (counter word 0 = pos / block), so whole blocks are kept in
  *     order of their draw and at most one block is split, at its lowest
@@ -286,8 +317,9 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *     out = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Slot order does not matter (rows after hole filling included).  A request
  * with no rows gets out = 0 and lse = -inf.
+ * Over a KVC_INT4 cache k_j and v_j are the values that the codes stand for.
  *   q:   device [layer_count][num_requests][num_q_heads][head_dim] in the
- *        cache dtype, element-aligned; read only.
+ *        cache dtype (bf16 for KVC_INT4), element-aligned; read only.
  *   scale: > 0, or 0 for 1/sqrt(head_dim).
  *   out: device float [layer_count][num_requests][num_q_heads][head_dim].
  *   lse: device float [layer_count][num_requests][num_q_heads] or NULL
@@ -296,10 +328,49 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *     the device time of its kernels, and reports latched device errors.
  * Enqueued on the context's stream; uses the context's workspace for split
  * partials, so calls on one context must not overlap.  Errors (nothing
- * enqueued): KVC_ERR_INVALID_ARG; KVC_ERR_UNSUPPORTED unless the cache is
- * bf16 or f32 with head_dim 64 or 128 and G in {1, 2, 4, 8}. */
+ * enqueued): KVC_ERR_INVALID_ARG; KVC_ERR_UNSUPPORTED unless head_dim is 64
+ * or 128 and G in {1, 2, 4, 8}. */
 kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,
                                 float scale, float *out, float *lse, float *ms_out);
+
+/* Options of a decode step (kvc_decode_attention_ex).  The all-default value,
+ * {0, 1, {0, 0}}, is the step of kvc_decode_attention.
+ *   accumulate: 1 adds each cached row's attention weight to the tracked
+ *     weights (KVC_ERR_STATE unless kvc_bind_weights has been called): for
+ *     every row j < length(r) of the listed layers and each KV head h,
+ *         w_j <- decay * w_j + sum over the G query heads g of h of
+ *                              exp(s_gj - lse_g).
+ *     A step adds G per (request, layer, KV head) in all.  Rows past a
+ *     request's length are left as they are.
+ *   decay: in [0, 1]; 1 gives the plain sum over the steps, 0 the last step's
+ *     weights.  Ignored without accumulate.
+ *   reserved: 0. */
+typedef struct kvc_attention_options {
+  int32_t accumulate;
+  float decay;
+  int32_t reserved[2];
+} kvc_attention_options;
+
+/* kvc_decode_attention with options; opts NULL means the defaults.  The sums
+ * run in a fixed order: the same state and queries give the same bits.
+ * Invalid options return KVC_ERR_INVALID_ARG with nothing enqueued. */
+kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,
+                                   float scale, const kvc_attention_options *opts, float *out, float *lse,
+                                   float *ms_out);
+
+/* Gives the context a buffer for accumulated attention weights, the scores of
+ * KVC_SEL_ATTENTION.
+ *   weights: device float [num_layers][num_pages][num_kv_heads][16], indexed
+ *     like the position map, 16-byte aligned, borrowed until the context is
+ *     destroyed or another buffer is bound; NULL stops the tracking.
+ *   weights_bytes: its size, at least that array's.
+ * The call sets every weight to 0 (enqueued).  From then on kvc_append starts
+ * new rows at 0, rounds move the weights with their rows, and
+ * kvc_decode_attention_ex adds to them; the caller may read or write them in
+ * stream order, for instance where another attention backend supplies them.
+ * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_UNSUPPORTED unless head_dim is 64 or
+ * 128. */
+kvc_status kvc_bind_weights(kvc_ctx *ctx, float *weights, size_t weights_bytes);
 
 /* Fills *out with device pointers to the live state (no copy, no sync). */
 kvc_status kvc_gather_view(const kvc_ctx *ctx, kvc_view *out);
@@ -310,6 +381,7 @@ kvc_status kvc_get_lengths(const kvc_ctx *ctx, int32_t *lengths, int32_t *prompt
 
 /* Dense copy of one layer for requests [req_begin, req_begin+req_count):
  *   k_out, v_out: device [req_count][num_kv_heads][cap][head_dim] dtype
+ *                 (KVC_INT4: float, the values the codes stand for)
  *   pos_out:      device [req_count][num_kv_heads][cap] int32
  * Slot j < min(length, cap) receives the row in slot j; the rest is zero
  * (pos -1).  Any output may be NULL. */

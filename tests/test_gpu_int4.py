@@ -1,0 +1,350 @@
+"""The 4-bit cache: its rows bit for bit, decode attention over them, rounds that move them.
+
+Tolerance of the attention (u = 2^-24).  The operands q and step*code have at most 8 significant bits each, so their
+products are exact in fp32; the tensor cores add 16 of them to an fp32 accumulator and may truncate, so each of the
+d/16 + 1 additions errs by at most 2u of the magnitudes it holds.  The group sums of q that multiply lo are fp32 sums of
+at most 32 terms, and scaling, the running maximum's subtraction and exp2 add three roundings.  With
+A = max_j scale*(sum_i |q_i| step code_ji + sum_g |lo_jg| sum_{i in g} |q_i|):
+  score error  ds <= (2*(d/16 + 1) + 8) * 2u * A + 2u*|s - m| + 4u.
+A weight enters the second product as the sum of two bf16 numbers, off by at most 2^-9 * 2^-9 = 2^-18 of itself (the
+normaliser adds the same rounded weights); its sums take L/16 additions of 2u each in one chain at most, the merges of
+the warps and CTAs 64 more roundings.  The product's terms are step*code and lo, at most 3 max|v| together:
+  out error    <= 3 max_j|v_jc| * (2 ds + 2 * 2^-18 + 2*(L/16 + 64)*2u),
+  lse error    <= ds + 2^-18 + (L/16 + 64)*2u + 4u|lse|."""
+import numpy as np
+import pytest
+import torch
+
+import rows4
+from decode_kv_cache_paged_b200 import KVC_ERR_STATE, KVC_ERR_UNSUPPORTED, Context, ContextSpec, KvcError
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def make(lens, layers=1, H=2, G=1, d=128, dtype="int4", extra_pages=4, room=0, window=0, device="cuda"):
+    longest = max(max(lens) + room, 16)
+    spec = ContextSpec(num_requests=len(lens), num_layers=layers, num_kv_heads=H, head_dim=d,
+                       max_seq_len=(longest + 15) // 16 * 16, num_q_heads=H * G, query_window=window,
+                       num_pages=sum((n + room + 15) // 16 for n in lens) + extra_pages)
+    return Context(spec, dtype=dtype, device=device)
+
+
+def rows(n, layers, H, d, seed, kind="normal", dtype=torch.bfloat16):
+    """K (or V) rows [1, layers, n, H, d]."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((1, layers, n, H, d), generator=g, device="cuda")
+    if kind == "hot":
+        x[..., 3::d // 4] *= 8
+    elif kind == "ties":  # steps of 1 and values on halves: every other code is a tie
+        x = torch.randint(0, 31, x.shape, generator=g, device="cuda") / 2
+        x[..., 0::d // 4] = 0
+        x[..., 1::d // 4] = 15
+    elif kind == "offset":
+        x = x * 0.25 + 100
+    elif kind == "constant":
+        x = x[..., :1].expand(x.shape).contiguous()
+    elif kind == "zero":
+        x = torch.zeros_like(x)
+    elif kind == "wide":
+        x = x * 2.0 ** torch.randint(-60, 60, x.shape[:-1] + (1,), generator=g, device="cuda")
+    elif kind == "edge":  # ranges around the smallest step and the largest one
+        e = torch.randint(0, 4, x.shape[:-1] + (1,), generator=g, device="cuda")
+        x = torch.where(e == 0, x * 2.0 ** -98, torch.where(e == 1, x * 2.0 ** -115, torch.where(e == 2, x * 2.0 ** 102, x * 2.0 ** 108)))
+    elif kind == "broken":
+        bad = torch.randint(0, 200, x.shape, generator=g, device="cuda")
+        x = torch.where(bad == 0, float("inf"), torch.where(bad == 1, float("-inf"), torch.where(bad == 2, float("nan"), x)))
+    return x.to(dtype)
+
+
+def fill(ctx, lens, seed=0, kind="hot", chunk=None):
+    """Appends lens[i] rows to request i; returns the K and V rows given, per request [layers, n, H, d]."""
+    s, out = ctx.spec, []
+    for i, n in enumerate(lens):
+        k = rows(n, s.num_layers, s.num_kv_heads, s.head_dim, seed + 10 * i, kind, ctx.dtype)
+        v = rows(n, s.num_layers, s.num_kv_heads, s.head_dim, seed + 10 * i + 5, kind, ctx.dtype)
+        step = chunk or max(n, 1)
+        for t in range(0, n, step):
+            ctx.append([i], k[:, :, t:t + step].contiguous(), v[:, :, t:t + step].contiguous())
+        out.append((k[0], v[0]))
+    return out
+
+
+def np64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", ["normal", "hot", "ties", "offset", "constant", "zero", "wide", "edge", "broken"])
+def test_values_are_the_definitions(d, kind):
+    """gather_dense returns exactly what the definition says, for every kind of row."""
+    lens = [37, 1, 0, 64]
+    ctx = make(lens, layers=2, H=3, d=d)
+    given = fill(ctx, lens, seed=3, kind=kind, chunk=13)
+    for layer in range(2):
+        k, v, pos = ctx.gather_dense(layer)
+        assert k.dtype == torch.float32
+        for i, n in enumerate(lens):
+            for got, x in ((k, given[i][0]), (v, given[i][1])):
+                want = rows4.row_values(np64(x[layer]).transpose(1, 0, 2))
+                have = got[i, :, :n].cpu().numpy()
+                assert np.array_equal(np.isnan(have), np.isnan(want))
+                assert np.array_equal(have[~np.isnan(want)], want[~np.isnan(want)].astype(np.float32))
+                assert not got[i, :, n:].any()
+            assert np.array_equal(pos[i, :, :n].cpu().numpy(), np.tile(np.arange(n), (3, 1)))
+            assert (pos[i, :, n:] == -1).all()
+    ctx.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_bytes_are_the_documented_ones(d):
+    ctx = make([20], H=2, d=d)
+    (k, v), = fill(ctx, [20], seed=8)
+    assert ctx.view().row_bytes == d // 2 + 16 == ctx.k_pool.shape[-1]
+    bt = ctx.state_tensors()["block_table"].cpu()
+    for pool, x in ((ctx.k_pool, k), (ctx.v_pool, v)):
+        step, lo, codes = rows4.code_rows(np64(x[0]).transpose(1, 0, 2))
+        for j in (0, 15, 16, 19):
+            raw = pool[0, int(bt[0, j // 16]), :, j % 16].cpu().numpy()  # [H, row bytes]
+            head = raw[:, :16].copy().view(np.uint32)
+            assert np.array_equal((head << 16).view(np.float32), step[:, j].astype(np.float32))
+            assert np.array_equal((head & 0xFFFF0000).view(np.float32), lo[:, j].astype(np.float32))
+            c = codes[:, j].reshape(2, d).astype(np.uint8)
+            assert np.array_equal(raw[:, 16:], c[:, 0::2] | (c[:, 1::2] << 4))
+    ctx.close()
+
+
+def test_host_rows_and_ring_queries():
+    """Rows from page-locked host memory; the query ring keeps bf16 queries."""
+    ctx = make([40], H=2, G=4, d=64, window=8)
+    k, v = (rows(40, 1, 2, 64, s).cpu().pin_memory() for s in (1, 2))
+    q = rows(40, 1, 8, 64, 3)
+    ctx.append([0], k, v, q)
+    got = ctx.gather_dense(0)[0][0].cpu().numpy()[:, :40]
+    assert np.array_equal(got, rows4.row_values(np64(k[0, 0]).transpose(1, 0, 2)).astype(np.float32))
+    ring = ctx.state_tensors()["query_ring"][0, 0]
+    assert torch.equal(ring, q[0, 0, 32:])  # slot = step mod 8
+    ctx.close()
+
+
+def check_attention(ctx, q, out, lse, layers, scale, tag=""):
+    s = ctx.spec
+    lens, _ = ctx.lengths()
+    d, G = s.head_dim, s.num_q_heads // s.num_kv_heads
+    worst = 0.0
+    for li, layer in enumerate(layers):
+        k, v, _ = ctx.gather_dense(layer, cap=int(max(lens.max(), 1)))
+        for r, L in enumerate(lens):
+            if L == 0:
+                assert not out[li, r].any() and torch.isneginf(lse[li, r]).all(), tag
+                continue
+            for h in range(s.num_kv_heads):
+                qq = np64(q[li, r, h * G:(h + 1) * G])
+                kk, vv = np64(k[r, h, :L]), np64(v[r, h, :L])
+                o, ll, _ = rows4.attention(qq, kk, vv, scale)
+                lo = np.repeat(kk.reshape(L, 4, -1).min(-1), d // 4, -1)  # at least the group's lo in size, with 15 steps
+                A = scale * (np.abs(qq) @ (np.abs(kk - lo) + np.abs(lo)).T)
+                ss = scale * (qq @ kk.T)
+                ds = (2 * (d / 16 + 1) + 8) * 2 * U * A.max(-1) + 2 * U * (ss.max(-1) - ss.min(-1)) + 4 * U
+                chain = (L / 16 + 64) * 2 * U
+                tol = 3 * np.abs(vv).max(0) * (2 * ds + 2 * 2.0 ** -18 + 2 * chain)[:, None] + 1e-30
+                err = np.abs(np64(out[li, r, h * G:(h + 1) * G]) - o)
+                assert np.all(err <= tol), (tag, layer, r, h, float((err / tol).max()))
+                le = np.abs(np64(lse[li, r, h * G:(h + 1) * G]) - ll)
+                assert np.all(le <= ds + 2.0 ** -18 + chain + 4 * U * np.abs(ll)), (tag, layer, r, h, float(le.max()))
+                worst = max(worst, float((err / tol).max()))
+    return worst
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 64, 65, 253, 1027]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_attention(G, d):
+    ctx = make(LENS, layers=2, H=2, G=G, d=d)
+    fill(ctx, LENS, seed=20)
+    q = rows(len(LENS), 2, 2 * G, d, 5)[0]  # [layers, R, Hq, d]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, range(2), d ** -0.5))
+    ctx.close()
+
+
+@pytest.mark.parametrize("lens", [[4133], [9001, 40], [32768]], ids=str)
+def test_attention_long(lens):
+    ctx = make(lens, H=2, G=4)
+    fill(ctx, lens, seed=30)
+    q = rows(len(lens), 1, 8, 128, 6)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
+    ctx.close()
+
+
+def test_attention_many_units():
+    """More (layer, request, KV head) units than CTAs fit at a time; a subset of the layers; a scale."""
+    lens = [100 + 13 * i for i in range(40)]
+    ctx = make(lens, layers=4, H=8, G=4, d=64)
+    fill(ctx, lens, seed=40)
+    q = rows(len(lens), 2, 32, 64, 7)[0]
+    out, lse = ctx.decode_attention(q, layer_begin=1, scale=0.3)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [1, 2], 0.3))
+    ctx.close()
+
+
+@pytest.mark.parametrize("kind", ["wide", "offset", "constant", "zero"])
+def test_attention_value_ranges(kind):
+    """Keys and values far from 1: the sums stay finite and within the bound."""
+    lens = [70, 300]
+    ctx = make(lens, H=2, G=4)
+    s = ctx.spec
+    for i, n in enumerate(lens):
+        k = rows(n, 1, 2, 128, 50 + i, "hot" if kind == "wide" else kind)
+        ctx.append([i], k, rows(n, 1, 2, 128, 60 + i, kind))
+    q = rows(2, 1, 8, 128, 9)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
+    assert torch.isfinite(out).all()
+    del s
+    ctx.close()
+
+
+def test_sharp_scores():
+    """Scores hundreds apart: the running maximum moves by far more than a step, up and down."""
+    lens = [600]
+    ctx = make(lens, H=2, G=4)
+    k = rows(600, 1, 2, 128, 70)
+    k[:, :, 77] *= 20
+    k[:, :, 399] *= 60
+    ctx.append([0], k, rows(600, 1, 2, 128, 71))
+    q = rows(1, 1, 8, 128, 10)[0] * 4
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
+    ctx.close()
+
+
+def test_what_lies_past_the_rows_does_not_matter():
+    """Garbage (NaN steps among it) behind the last row of a page, and in free pages, changes no bit."""
+    lens = [5, 33, 250]
+    q = rows(3, 1, 8, 128, 11)[0]
+    got = []
+    for junk in (0, 255):
+        ctx = make(lens, H=2, G=4)
+        ctx.k_pool.fill_(junk)
+        ctx.v_pool.fill_(junk)
+        fill(ctx, lens, seed=80)
+        got.append(ctx.decode_attention(q))
+        ctx.sync()
+        ctx.close()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][0]).all()
+
+
+def test_a_broken_group_shows_only_where_it_is_read():
+    """A NaN in one request's values leaves the other requests and KV heads as they were."""
+    lens = [40, 40]
+    ctx = make(lens, H=2, G=4)
+    k, v = rows(40, 1, 2, 128, 90), rows(40, 1, 2, 128, 91)
+    ctx.append([0], k, v)
+    v2 = v.clone()
+    v2[0, 0, 7, 1, 100] = float("nan")  # group 3 of KV head 1
+    ctx.append([1], k, v2)
+    q = rows(2, 1, 8, 128, 12)[0]
+    q[:, 1] = q[:, 0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    assert torch.equal(out[0, 0, :4], out[0, 1, :4]) and torch.equal(lse[0, 0], lse[0, 1])
+    assert torch.isnan(out[0, 1, 4:, 96:]).all()
+    assert torch.equal(out[0, 0, 4:, :96], out[0, 1, 4:, :96])
+    ctx.close()
+
+
+@pytest.mark.parametrize("compaction", ["ordered", "hole_fill"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rounds_move_whole_rows(d, compaction):
+    """After random rounds and appends every slot holds the values of the position that it names."""
+    lens = [200, 77, 5200]
+    ctx = make(lens, layers=2, H=2, d=d, room=32)
+    given = fill(ctx, lens, seed=100)
+    budgets = np.array([120, 64, 4096], np.int32)
+    more = [[], [], []]
+    for rnd in range(2):
+        ctx.compress("random", budgets - 16 * rnd, 5 + rnd, compaction=compaction)
+        k = rows(3 * 9, 2, 2, d, 200 + rnd).view(2, 3, 9, 2, d).transpose(0, 1).contiguous()
+        ctx.append([0, 1, 2], k, k)
+        for i in range(3):
+            more[i].append(k[i])
+    ctx.sync()
+    now, _ = ctx.lengths()
+    assert now.tolist() == [113, 57, 4089]
+    for layer in range(2):
+        gk, gv, gp = ctx.gather_dense(layer)
+        for i in range(3):
+            allk = np64(torch.cat([given[i][0]] + more[i], 1)[layer])  # [n, H, d] by position
+            allv = np64(torch.cat([given[i][1]] + more[i], 1)[layer])
+            for h in range(2):
+                pos = gp[i, h, :now[i]].cpu().numpy()
+                assert len(set(pos.tolist())) == now[i]
+                assert np.array_equal(gk[i, h, :now[i]].cpu().numpy(), rows4.row_values(allk[pos, h]).astype(np.float32))
+                assert np.array_equal(gv[i, h, :now[i]].cpu().numpy(), rows4.row_values(allv[pos, h]).astype(np.float32))
+    q = rows(3, 2, 2, d, 13)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, range(2), d ** -0.5))
+    ctx.close()
+
+
+def test_the_same_call_gives_the_same_bits():
+    ctx = make([3000, 10], H=2, G=8)
+    fill(ctx, [3000, 10], seed=110)
+    q = rows(2, 1, 16, 128, 14)[0]
+    a = ctx.decode_attention(q)
+    b = ctx.decode_attention(q)
+    ctx.sync()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ctx.close()
+
+
+def test_captured_step_follows_the_cache():
+    """A captured step replays over the cache as it then stands: more rows, other queries."""
+    lens = [100, 900]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ctx = make(lens, H=2, G=4, room=2000)
+        fill(ctx, lens, seed=120)
+        q = rows(2, 1, 8, 128, 15)[0]
+        out, lse = ctx.decode_attention(q)  # the first call sets the kernels up
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            ctx.decode_attention(q, out=out, lse=lse)
+        fill(ctx, [1500, 700], seed=130)
+        q.copy_(rows(2, 1, 8, 128, 16)[0])
+        graph.replay()
+        side.synchronize()
+        print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
+        side.synchronize()
+    ctx.close()
+
+
+def test_refusals():
+    ctx = make([20], H=2, G=3)
+    q = rows(1, 1, 6, 128, 1)[0]
+    with pytest.raises(KvcError) as e:
+        ctx.decode_attention(q)
+    assert e.value.status == KVC_ERR_UNSUPPORTED
+    with pytest.raises(KvcError) as e:
+        ctx.compress("beacon", np.array([4], np.int32), 0)
+    assert e.value.status == KVC_ERR_STATE
+    with pytest.raises(KvcError):
+        ctx.update_beacons()
+    with pytest.raises(ValueError):
+        ctx.append([0], torch.zeros((1, 1, 2, 2, 128), device="cuda"), torch.zeros((1, 1, 2, 2, 128), device="cuda"))
+    with pytest.raises(ValueError):
+        ctx.decode_attention(q.float())
+    ctx.close()
