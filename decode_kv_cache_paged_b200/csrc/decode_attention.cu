@@ -41,8 +41,7 @@
 // leaves, all threads of the CTA together.
 #include <cuda_bf16.h>
 
-#include "kvc_internal.h"
-#include "tc_ptx.cuh"
+#include "attn_cluster.cuh"
 
 namespace kvc {
 namespace {
@@ -157,7 +156,10 @@ constexpr int ilog2(int x) { return x <= 1 ? 0 : 1 + ilog2(x / 2); }
 // Each of the 4 warps walks every 4th page of the CTA's split through its own
 // 2-slot ring (K and V of one page per slot), with its own running max and
 // sums; no block-wide barrier is taken until the warps' states are merged.
-template <typename T, int D, int G>
+// ACC: the step that accumulates attention weights.  A unit's splits are the
+// CTAs of a cluster, the base-2 scores stay in shared memory past the page
+// slots, and attn_cluster.cuh merges the CTAs and adds the weights.
+template <typename T, int D, int G, bool ACC>
 __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnParams p) {
   using S = AttnShape<T, D, G>;
   constexpr int W = S::kWarps, NS = S::kWarpStages, KEEP = S::kKeep;
@@ -169,18 +171,24 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   __shared__ __align__(8) uint64_t full[W][NS];
   __shared__ int abort_flag_s;
   volatile int *abort_flag = &abort_flag_s;
+  [[maybe_unused]] float *scores = reinterpret_cast<float *>(smem + S::kSmem - 128);  // [rows of this CTA][G] (ACC)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x;
-  const int split = unit % p.nsplit;
-  const int h = (unit / p.nsplit) % p.hkv;
-  const int r = (unit / (p.nsplit * p.hkv)) % p.R;
-  const int lc = unit / (p.nsplit * p.hkv * p.R);
-  const int l = p.layer_begin + lc;
-  const int len = p.lengths[r];
-  const int n_pages = (len + kPage - 1) / kPage;
-  const int pg0 = split * p.pages_per_split;
-  const int pg1 = min(n_pages, pg0 + p.pages_per_split);
+  AttnUnit un{};
+  if constexpr (ACC) {
+    un = attn_unit(p);
+  } else {
+    const int unit = blockIdx.x;
+    un.rank = unit % p.nsplit;
+    un.h = (unit / p.nsplit) % p.hkv;
+    un.r = (unit / (p.nsplit * p.hkv)) % p.R;
+    un.lc = unit / (p.nsplit * p.hkv * p.R);
+    un.l = p.layer_begin + un.lc;
+    un.len = p.lengths[un.r];
+    un.pg0 = un.rank * p.pages_per_split;
+    un.pg1 = min((un.len + kPage - 1) / kPage, un.pg0 + p.pages_per_split);
+  }
+  const int split = un.rank, h = un.h, r = un.r, lc = un.lc, l = un.l, len = un.len, pg0 = un.pg0, pg1 = un.pg1;
   const int n_my = pg1 - pg0 > warp ? (pg1 - pg0 - warp + W - 1) / W : 0;  // pages of this warp
   const int32_t *bt = p.block_table + (int64_t)r * p.bt_stride;
   uint8_t *ring = smem + warp * NS * S::kSlotBytes;
@@ -291,6 +299,17 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
       const int row = grp * S::kRowsPerGroup + b * S::kRb + e0 / G;
 #pragma unroll
       for (int kk = 0; kk < KEEP; ++kk) sv[b][kk] = row < valid ? part[kk] : -INFINITY;
+    }
+
+    if constexpr (ACC) {
+      if (writer) {
+#pragma unroll
+        for (int b = 0; b < S::kBatches; ++b) {
+          float *dst = scores + ((warp + k * W) * kPage + grp * S::kRowsPerGroup + b * S::kRb + e0 / G) * G + g0;
+#pragma unroll
+          for (int kk = 0; kk < KEEP; ++kk) dst[kk] = sv[b][kk];
+        }
+      }
     }
 
     // 2. online softmax per head: the max over the lanes holding that head
@@ -410,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
       }
   }
   __syncthreads();  // every warp is past its loop: the page slots are free
-  if (*abort_flag) return;
+  if (!ACC && *abort_flag) return;  // (the CTAs of a cluster leave together, through the merge)
   float *red = reinterpret_cast<float *>(smem);  // [W][G][D]
   if (vgrp == 0) {
 #pragma unroll
@@ -424,6 +443,11 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
       }
   }
   __syncthreads();
+  if constexpr (ACC) {
+    __shared__ AttnMerge mg;
+    attn_finish<D, W, kThreads>(p, un, G, red, &m_s[0][0], &l_s[0][0], mg, scores);
+    return;
+  }
   const int64_t head0 = ((int64_t)lc * p.R + r) * p.hq + (int64_t)h * G;  // first query head row
   for (int i = tid; i < G * D; i += kThreads) {
     const int g = i / D;
@@ -480,11 +504,28 @@ __global__ void __launch_bounds__(kThreads) decode_attention_merge_kernel(Decode
 template <typename T, int D, int G>
 cudaError_t launch_typed(const DecodeAttnParams &p, int units, cudaStream_t s) {
   using S = AttnShape<T, D, G>;
-  cudaError_t e = cudaFuncSetAttribute(decode_attention_kernel<T, D, G>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  auto kernel = decode_attention_kernel<T, D, G, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
-  decode_attention_kernel<T, D, G><<<units, kThreads, S::kSmem, s>>>(p);
+  kernel<<<units, kThreads, S::kSmem, s>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_acc(DecodeAttnParams p, int np_max, int sms, cudaStream_t s) {
+  auto kernel = decode_attention_kernel<T, D, G, true>;
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, AttnShape<T, D, G>::kSmem,
+                             (size_t)kPage * G * 4, kThreads, s);
+}
+
+template <typename T, int D>
+cudaError_t launch_acc_g(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
+  switch (G) {
+    case 1: return launch_acc<T, D, 1>(p, np_max, sms, s);
+    case 2: return launch_acc<T, D, 2>(p, np_max, sms, s);
+    case 4: return launch_acc<T, D, 4>(p, np_max, sms, s);
+    default: return launch_acc<T, D, 8>(p, np_max, sms, s);
+  }
 }
 
 template <typename T, int D>
@@ -500,8 +541,16 @@ cudaError_t launch_g(const DecodeAttnParams &p, int G, int units, cudaStream_t s
 }  // namespace
 
 bool decode_attention_supported(int dtype, int head_dim, int G) {
-  return (dtype == KVC_BF16 || dtype == KVC_F32) && (head_dim == 64 || head_dim == 128) &&
+  return (dtype == KVC_BF16 || dtype == KVC_F32 || dtype == KVC_INT4) && (head_dim == 64 || head_dim == 128) &&
          (G == 1 || G == 2 || G == 4 || G == 8);
+}
+
+cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, int np_max, int sms,
+                                        cudaStream_t s) {
+  if (dtype == KVC_BF16)
+    return head_dim == 128 ? launch_acc_g<__nv_bfloat16, 128>(p, G, np_max, sms, s)
+                           : launch_acc_g<__nv_bfloat16, 64>(p, G, np_max, sms, s);
+  return head_dim == 128 ? launch_acc_g<float, 128>(p, G, np_max, sms, s) : launch_acc_g<float, 64>(p, G, np_max, sms, s);
 }
 
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,

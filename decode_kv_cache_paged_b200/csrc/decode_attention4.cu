@@ -1,109 +1,645 @@
-// decode_attention4.cu -- decode attention over the 4-bit cache, and decode
-// attention that accumulates each cached row's attention weight.
+// decode_attention4.cu -- one decode step of grouped-query attention over the
+// 4-bit cache (KVC_INT4), with or without accumulating the rows' attention
+// weights.
+//
+// What it computes: as decode_attention.cu, with k_j and v_j the values that
+// the codes of int4.cuh stand for.
+//
+// Design (B200).  A cached row is 80 bytes (D = 128) against 256 in bf16, so
+// at the HBM rate an SM meets a page of 16 rows (2.5 KB of K and V) every 100
+// clocks: 400 issue slots in which 4096 codes become operands of 2 * 4096 * G
+// products.  The CUDA cores alone need more than that for the products, and
+// feeding tcgen05 would cost a write and a read of the decoded page through
+// shared memory (8 KB each way, 160 clocks of its port).  So the codes are
+// decoded in registers, straight into the fragments of warp-level mma with the
+// rows on M and the query heads on N:
+//   S^T[16 rows x 8] = K . Q^T per group       m16n8k16, fp16
+//   O^T[D x 8]      += V^T . P^T               m16n8k16, bf16
+// Which channel sits at which k of the first product, and which at which row
+// of the second, is free as long as both operands agree, so a lane reads its
+// codes where they lie and no transposing load is needed.  The logic pipe (one
+// and-or, shift or byte permute every two clocks per scheduler) is what the
+// decoding fills, so each form is chosen for the fewest of those:
+//   * K: the low and the high nibble of a byte, masked in place, are the fp16
+//     subnormals code * 2^-24 and code * 2^-20: a word of eight codes takes one
+//     shift and four ands, and nothing else.  The query is the other operand,
+//     scaled per head to |q| < 2048 and split into an integer and the rest, both
+//     fp16: the integers' products and sums are exact (the tensor cores
+//     truncate each product to the place of the largest, which costs 5e-6 of a
+//     score otherwise), those of the rest are too small to matter.  A group is
+//     a sum of its own, which s multiplies in fp32, where lo * the group's sum
+//     of q joins it.
+//     (8-bit floats would take fewer ands, but their products expand to fp16
+//     ones with a conversion per two codes: measured 24 instructions of the
+//     logic pipe more per page.)
+//   * V: the low and the high nibble of a byte, masked in place, are the bf16
+//     numbers code * 2^-133 and code * 2^-129 (linear from the subnormals
+//     through the first binade), so one byte permute and two ands make four operands, and
+//     one fma by (s * 2^69 or s * 2^65, -z s / 2^64) gives s (code - z) / 2^64
+//     exactly.  mid is one more product, with a row of ones beside it that
+//     gives the softmax's sum.
+//   * P enters as three bf16 terms, all of its 24 bits: two would leave 2^-17 of
+//     a weight, 1.2e-6 of an output where fp32 sums leave 3e-7.
+//   * With at most 4 query heads per KV head the two parts of q, and the first
+//     two terms of P, are columns 0..3 and 4..7 of one product, and the third
+//     term takes another; with 8 heads each takes one.
+//   * The running maximum is lazy: two pages' scores are compared with it and
+//     the sums are rescaled only when one exceeds it by more than 2^8, so a
+//     page needs no reduction across lanes.
+// Each warp walks its own pairs of pages through its own ring of slots, one
+// bulk copy each for the K and the V rows of a page.  The split over a cluster
+// and the merge are attn_cluster.cuh's.
+// Every mbarrier wait is bounded (tc_ptx.cuh).
 #include <cuda_bf16.h>
 
+#include "attn_cluster.cuh"
 #include "int4.cuh"
-#include "kvc_internal.h"
 
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr float kLn2 = 0.6931471805599453f;
+#ifndef KVC_ATTN4_WARPS
+#define KVC_ATTN4_WARPS 4
+#endif
+constexpr int kWarps = KVC_ATTN4_WARPS;
+constexpr int kThreads = 32 * kWarps;
 
-template <int DT>
-__device__ __forceinline__ float row_value(const uint8_t *row, int d, int c) {
-  if (DT == KVC_F32) return reinterpret_cast<const float *>(row)[c];
-  if (DT == KVC_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[c]);
-  const uint32_t h = *reinterpret_cast<const uint32_t *>(row + (c / (d / kInt4Groups)) * 4);
-  const int code = (row[kInt4Header + c / 2] >> (4 * (c & 1))) & 15;
-  return fmaf((float)code, __uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u));
+#ifndef KVC_ATTN4_STAGES
+#define KVC_ATTN4_STAGES 2
+#endif
+constexpr int kStages = KVC_ATTN4_STAGES;  // slots per warp
+#ifndef KVC_ATTN4_PAIR
+#define KVC_ATTN4_PAIR 2
+#endif
+constexpr int kPair = KVC_ATTN4_PAIR;      // pages per slot
+#ifndef KVC_ATTN4_MINB
+#define KVC_ATTN4_MINB 4
+#endif
+
+template <int D>
+struct Shape4 {
+  static constexpr int kRow = int4_row_bytes(D);
+  static constexpr int kPageBytes = kPage * kRow;     // K (or V) of one page
+  static constexpr int kSlot = kPair * 2 * kPageBytes;  // K, V of the first page, K, V of the second
+  static constexpr int kRing = kWarps * kStages * kSlot;
+  static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and K row
+  static constexpr int kTiles = D / 16;  // products per page on the V side
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = A . B without a sum to add to; bf16
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// fp16: d = A . B, and d += A . B
+__device__ __forceinline__ void mma16816h_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma16816h(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// (lo, hi) rounded to a bf16 pair, lo in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// One CTA per (layer, request, query head); with weights per (layer, request,
-// KV head), which then loops over its G query heads.
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) attend_kernel(DecodeAttnParams p, int G, int row_bytes) {
-  constexpr int W = kThreads / 32, E = D / 32;
-  __shared__ float m_s[W], l_s[W], o_s[W][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % p.hkv, r = (blockIdx.x / p.hkv) % p.R, lc = blockIdx.x / (p.hkv * p.R);
-  const int len = p.lengths[r];
-  const int32_t *bt = p.block_table + (int64_t)r * p.bt_stride;
-  const int64_t layer0 = (int64_t)(p.layer_begin + lc) * p.num_pages;
-  auto row_of = [&](int j) { return ((layer0 + bt[j / kPage]) * p.hkv + h) * kPage + j % kPage; };
-  for (int g = 0; g < G; ++g) {
-    const int64_t head = ((int64_t)lc * p.R + r) * p.hq + (int64_t)h * G + g;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[e] = row_value<DT == KVC_F32 ? KVC_F32 : KVC_BF16>(p.q + head * D * (DT == KVC_F32 ? 4 : 2), D, lane + 32 * e);
-      o[e] = 0.f;
+// s * 2^69, s * 2^65 and -z s / 2^64 of a pair of V rows, from their words' high halves
+__device__ __forceinline__ void unpack_steps(uint32_t r, uint32_t &s_lo, uint32_t &s_hi, uint32_t &off) {
+  const uint32_t s2 = r & 0xfff0fff0u;
+  s_lo = s2 + 0x22802280u;
+  s_hi = s2 + 0x20802080u;
+  off = mul_bf16x2(r & 0x000f000fu, s2 + 0xa280a280u);  // z * 2^-133 by -s * 2^69
+}
+constexpr uint32_t kOnes = 0x3f803f80u;
+constexpr float kLazy = 8.f;  // a score may exceed the running maximum by this much (base 2)
+
+// GP: columns of the product that hold query heads, 4 (G <= 4: the second parts
+// take the other four) or 8.  ACC: keep the scores and add the weights.
+template <int D, int GP, bool ACC>
+__global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_kernel(DecodeAttnParams p, int G) {
+  using S = Shape4<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_align<128>(smem_raw);
+  float *scores = reinterpret_cast<float *>(smem + S::kRing);  // [rows of this CTA][G] (ACC)
+  __shared__ float m_s[kWarps * 8], l_s[kWarps * 8];
+  __shared__ AttnMerge mg;
+  __shared__ __align__(8) uint64_t full[kWarps][kStages];
+  __shared__ int abort_flag_s;
+  volatile int *abort_flag = &abort_flag_s;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = lane >> 2, t = lane & 3;  // a fragment's row and column index of this lane
+  const AttnUnit u = attn_unit(p);
+  // this warp's pairs of pages: u.pg0 + 2 (warp + k * kWarps), the last one maybe half
+  const int n_pages = u.pg1 - u.pg0, first = u.pg0 + kPair * warp;
+  const int n_my = n_pages > kPair * warp ? (n_pages - kPair * warp + kPair * kWarps - 1) / (kPair * kWarps) : 0;
+  const int rows_end = min(u.len, u.pg1 * kPage);
+  uint8_t *ring = smem + warp * kStages * S::kSlot;
+
+  if (tid == 0) {
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kStages; ++i) mbar_init(&full[w][i], 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  // page ids of this warp's pages, 32 at a time, one per lane; the next 32
+  // are on their way before they are needed
+  auto load_ids = [&](int k0) {
+    const int pg = first + (k0 + lane / kPair) * kPair * kWarps + lane % kPair;
+    return pg < u.pg1 ? u.bt[pg] : -1;
+  };
+  int ids = load_ids(0), ids_next = load_ids(32 / kPair);
+  int ids_base = 0;
+  const uint32_t ring_u = smem_u32(ring);
+  const int page_stride = p.hkv * S::kPageBytes;  // bytes from a page to the next in a pool
+  const uint8_t *pool = ((lane & 1) ? p.v_pool : p.k_pool) +
+                        ((int64_t)u.l * p.num_pages * p.hkv + u.h) * S::kPageBytes;  // page 0 of this unit
+  auto issue_pair = [&](int k) {
+    if (k >= ids_base + 32 / kPair) {
+      ids = ids_next;
+      ids_base += 32 / kPair;
+      ids_next = load_ids(ids_base + 32 / kPair);
     }
-    auto score = [&](int64_t row) {
-      float s = 0.f;
+    const int slot = k % kStages;
+    // lanes 0..3 copy K, V of the first page, K, V of the second
+    const int id = __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + (lane >> 1) % kPair);
+    const bool both = kPair == 1 || __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + kPair - 1) >= 0;
+    if (lane == 0) mbar_expect_tx(&full[warp][slot], (uint32_t)(both ? S::kSlot : S::kSlot / 2));
+    __syncwarp();
+    if (lane < (both ? 2 * kPair : 2))
+      bulk_load(ring_u + slot * S::kSlot + lane * S::kPageBytes, pool + (int64_t)id * page_stride,
+                (uint32_t)S::kPageBytes, &full[warp][slot]);
+  };
+  for (int k = 0; k < min(n_my, kStages); ++k) issue_pair(k);
+
+  // query fragments.  Column n: head n & 3, its integers in columns 0..3 and the
+  // rest in 4..7 (GP = 4), or head n with the two parts in two tiles (GP = 8); a
+  // smaller group repeats.  Products 2 gr and 2 gr + 1 are group gr's, with this
+  // lane's unit t of it: low nibbles first, then high ones (times 2^-4: their
+  // codes are 2^4 larger).
+  constexpr int kQt = GP == 4 ? 1 : 2;
+  uint32_t qb[kQt][2 * kInt4Groups][2];
+  // sums of q beside lo, columns 2t and 2t + 1.  GP = 4: lanes t and t ^ 2 hold
+  // the same heads and are added later, so each takes two groups, from 2 (t / 2).
+  constexpr int kLo = GP == 4 ? 2 : kInt4Groups;
+  float qsum[kLo][2];
+  float lam0, lam1;  // from a column's sum to base-2 scores, columns 2t and 2t + 1
+  {
+    const int g = (GP == 4 ? n & 3 : n) % G;
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) +
+                        ((((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G + g) * D + t * (D / 16));
+    float x[kInt4Groups][D / 16], top = 0.f, bad = 0.f, sum[kInt4Groups];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], row_value<DT>(p.k_pool + row * row_bytes, D, lane + 32 * e), s);
+    for (int gr = 0; gr < kInt4Groups; ++gr)
 #pragma unroll
-      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      return s * p.qscale;
-    };
-    for (int j = warp; j < len; j += W) {
-      const int64_t row = row_of(j);
-      const float s = score(row), mn = fmaxf(m, s);
-      const float a = exp2f(m - mn), w = exp2f(s - mn);
-      m = mn;
-      l = l * a + w;
+      for (int i = 0; i < D / 16; ++i) {
+        x[gr][i] = bf16_lo(q[gr * (D / 4) + i]);
+        top = fmaxf(top, fabsf(x[gr][i]));
+        bad = fmaf(x[gr][i], 0.f, bad);  // NaN once a query value is infinite or NaN
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    bad += __shfl_xor_sync(0xffffffffu, bad, 1);
+    bad += __shfl_xor_sync(0xffffffffu, bad, 2);
+    // sigma: the power of two that brings the head's largest |q| into [1024, 2048)
+    const int ex = max(-120, min(100, 137 - (int)(__float_as_uint(top) >> 23)));
+    const float sigma = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        o[e] = o[e] * a + w * row_value<DT>(p.v_pool + row * row_bytes, D, lane + 32 * e);
+    for (int gr = 0; gr < kInt4Groups; ++gr) {
+      sum[gr] = bad;
+      float part[2][D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const float v = x[gr][i] * sigma;
+        sum[gr] += v;
+        part[0][i] = rintf(v);
+        part[1][i] = v - part[0][i];
+      }
+#pragma unroll
+      for (int z = 0; z < kQt; ++z) {
+        float c[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) c[i] = (GP == 4 ? n >= 4 : z == 1) ? part[1][i] : part[0][i];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if constexpr (D == 128) {  // codes i and i + 4 of a word share a register
+            qb[z][2 * gr + y][0] = pack_f16(c[2 * y], c[2 * y + 4]);
+            qb[z][2 * gr + y][1] = pack_f16(c[2 * y + 1] * 0.0625f, c[2 * y + 5] * 0.0625f);
+          } else {  // codes i of two groups share one: the other group's place is 0
+            const float a = c[2 * y], b = c[2 * y + 1] * 0.0625f;
+            qb[z][2 * gr + y][0] = (gr & 1) ? pack_f16(0.f, a) : pack_f16(a, 0.f);
+            qb[z][2 * gr + y][1] = (gr & 1) ? pack_f16(0.f, b) : pack_f16(b, 0.f);
+          }
+        }
+      }
+      sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+      sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+      sum[gr] *= 0x1p-24f;  // the codes' unit
     }
-    if (lane == 0) {
-      m_s[warp] = m;
-      l_s[warp] = l;
-    }
+    // column c's values sit with lanes n = c
 #pragma unroll
-    for (int e = 0; e < E; ++e) o_s[warp][lane + 32 * e] = o[e];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
-    for (int w = 0; w < W; ++w)
-      if (l_s[w] != 0.f) L += l_s[w] * exp2f(m_s[w] - M);
-    for (int c = threadIdx.x; c < D; c += kThreads) {
-      float v = 0.f;
-      for (int w = 0; w < W; ++w)
-        if (l_s[w] != 0.f) v += o_s[w][c] * exp2f(m_s[w] - M);
-      p.out[head * D + c] = len > 0 ? v / L : 0.f;
+    for (int i = 0; i < kLo; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float a = __shfl_sync(0xffffffffu, sum[i], (2 * t + x) * 4);
+        if constexpr (GP == 4) {
+          const float b = __shfl_sync(0xffffffffu, sum[i + 2], (2 * t + x) * 4);
+          qsum[i][x] = t >= 2 ? b : a;
+        } else {
+          qsum[i][x] = a;
+        }
+      }
+    const float lam = p.qscale * 0x1p24f * __uint_as_float((uint32_t)(127 - ex) << 23);
+    lam0 = __shfl_sync(0xffffffffu, lam, (2 * t) * 4);
+    lam1 = __shfl_sync(0xffffffffu, lam, (2 * t + 1) * 4);
+  }
+
+  constexpr int kPt = GP == 4 ? 2 : 3;  // products for the terms of P
+  // rows of a page: fragment rows n and n + 8 are page rows ra and ra + 1, an
+  // order in which no two lanes of a shared-memory phase meet in a bank
+  const int ra = (n & 1) ? ((n + 3) & 7) + 8 : n;
+  const int v0 = 2 * t, v1 = ((2 * t + 4) & 7) + 8;  // P's rows 2t and 2t + 1; v0 + 1 and v1 + 1 are 2t + 8 and 2t + 9
+
+  float m0 = -INFINITY, m1 = -INFINITY;  // running maxima of columns 2t and 2t + 1 (base 2)
+  float o[S::kTiles][4], e[4];  // e: the mid term (rows n), the sum of P (rows n + 8)
+#pragma unroll
+  for (int i = 0; i < S::kTiles; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) e[x] = 0.f;
+
+  int k = 0;
+  for (; k < n_my; ++k) {
+    const int slot = k % kStages;
+    const uint32_t parity = (uint32_t)((k / kStages) & 1);
+    if (__any_sync(0xffffffffu, !mbar_try(&full[warp][slot], parity)) &&
+        __any_sync(0xffffffffu, !mbar_wait(&full[warp][slot], parity, abort_flag, p.status)))
+      break;
+    const uint8_t *base = ring + slot * S::kSlot;
+    const int valid = rows_end - (first + k * kPair * kWarps) * kPage;  // rows here; what lies past them is anything
+
+    // 1. base-2 scores: s[y][0..1] of page row ra, [2..3] of row ra + 1, for columns 2t, 2t + 1
+    float s[kPair][4];
+#pragma unroll
+    for (int y = 0; y < kPair; ++y) {
+      const uint8_t *row0 = base + y * 2 * S::kPageBytes + ra * S::kRow, *row1 = row0 + S::kRow;
+      const uint4 h0 = *reinterpret_cast<const uint4 *>(row0), h1 = *reinterpret_cast<const uint4 *>(row1);
+      const uint32_t ga[4] = {h0.x, h0.y, h0.z, h0.w}, gb[4] = {h1.x, h1.y, h1.z, h1.w};
+      uint32_t wa[S::kWords], wb[S::kWords];
+      if constexpr (S::kWords == 4) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row0 + kInt4Header + t * 16);
+        const uint4 b = *reinterpret_cast<const uint4 *>(row1 + kInt4Header + t * 16);
+        wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
+        wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
+      } else {
+        const uint2 a = *reinterpret_cast<const uint2 *>(row0 + kInt4Header + t * 8);
+        const uint2 b = *reinterpret_cast<const uint2 *>(row1 + kInt4Header + t * 8);
+        wa[0] = a.x, wa[1] = a.y;
+        wb[0] = b.x, wb[1] = b.y;
+      }
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      // lo by the sums of q
+      uint32_t ka[kLo], kb[kLo];
+      if constexpr (GP == 4) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(row0 + (t >> 1) * 8);
+        const uint2 b = *reinterpret_cast<const uint2 *>(row1 + (t >> 1) * 8);
+        ka[0] = a.x, ka[1] = a.y, kb[0] = b.x, kb[1] = b.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLo; ++i) ka[i] = ga[i], kb[i] = gb[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kLo; ++i) {
+        acc[0] = fmaf(bf16_lo(ka[i]), qsum[i][0], acc[0]);
+        acc[1] = fmaf(bf16_lo(ka[i]), qsum[i][1], acc[1]);
+        acc[2] = fmaf(bf16_lo(kb[i]), qsum[i][0], acc[2]);
+        acc[3] = fmaf(bf16_lo(kb[i]), qsum[i][1], acc[3]);
+      }
+#pragma unroll
+      for (int gr = 0; gr < kInt4Groups; ++gr) {
+        const uint32_t a = wa[D == 128 ? gr : gr / 2], b = wb[D == 128 ? gr : gr / 2];
+        const uint32_t a0 = a & 0x000f000fu, a1 = a & 0x00f000f0u, a2 = a >> 8 & 0x000f000fu, a3 = a >> 8 & 0x00f000f0u;
+        const uint32_t b0 = b & 0x000f000fu, b1 = b & 0x00f000f0u, b2 = b >> 8 & 0x000f000fu, b3 = b >> 8 & 0x00f000f0u;
+        const float sa = __uint_as_float(ga[gr] & 0xfff00000u), sb = __uint_as_float(gb[gr] & 0xfff00000u);
+#pragma unroll
+        for (int z = 0; z < kQt; ++z) {
+          float d[4];
+          mma16816h_zero(d, a0, b0, a1, b1, qb[z][2 * gr][0], qb[z][2 * gr][1]);
+          mma16816h(d, a2, b2, a3, b3, qb[z][2 * gr + 1][0], qb[z][2 * gr + 1][1]);
+          acc[0] = fmaf(sa, d[0], acc[0]);
+          acc[1] = fmaf(sa, d[1], acc[1]);
+          acc[2] = fmaf(sb, d[2], acc[2]);
+          acc[3] = fmaf(sb, d[3], acc[3]);
+        }
+      }
+      s[y][0] = acc[0] * lam0;
+      s[y][1] = acc[1] * lam1;
+      s[y][2] = acc[2] * lam0;
+      s[y][3] = acc[3] * lam1;
+      if constexpr (GP == 4)  // the columns with the other part
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[y][x] += __shfl_xor_sync(0xffffffffu, s[y][x], 2);
     }
-    const float lse2 = M + log2f(L);
-    if (p.lse && threadIdx.x == 0) p.lse[head] = len > 0 ? lse2 * kLn2 : -INFINITY;
-    if (p.weights) {
-      for (int j = warp; j < len; j += W) {
-        const int64_t row = row_of(j);
-        const float w = exp2f(score(row) - lse2);
-        if (lane == 0) p.weights[row] = (g == 0 ? p.decay : 1.f) * p.weights[row] + w;
+    if (valid < kPair * kPage) {
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        if (y * kPage + ra >= valid) s[y][0] = s[y][1] = -INFINITY;
+        if (y * kPage + ra + 1 >= valid) s[y][2] = s[y][3] = -INFINITY;
       }
     }
-    __syncthreads();
+    if constexpr (ACC) {
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        // the buffer holds whole pages: the second page of the last pair may lie past it
+        if (y * kPage >= valid) continue;
+        float *dst = scores + ((kPair * (warp + k * kWarps) + y) * kPage + ra) * G + 2 * t;
+        if (2 * t < G) {
+          dst[0] = s[y][0];
+          dst[G] = s[y][2];
+        }
+        if (2 * t + 1 < G) {
+          dst[1] = s[y][1];
+          dst[G + 1] = s[y][3];
+        }
+      }
+    }
+
+    // 2. lazy running maximum
+    float c0 = fmaxf(s[0][0], s[0][2]), c1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+    for (int y = 1; y < kPair; ++y) {
+      c0 = fmaxf(c0, fmaxf(s[y][0], s[y][2]));
+      c1 = fmaxf(c1, fmaxf(s[y][1], s[y][3]));
+    }
+    if (__any_sync(0xffffffffu, c0 > m0 + kLazy || c1 > m1 + kLazy)) {
+      float n0 = fmaxf(c0, m0), n1 = fmaxf(c1, m1);
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+      }
+      const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);  // n0, n1 > -inf: a slot has a row
+      m0 = n0;
+      m1 = n1;
+#pragma unroll
+      for (int i = 0; i < S::kTiles; ++i) {
+        o[i][0] *= a0;
+        o[i][1] *= a1;
+        o[i][2] *= a0;
+        o[i][3] *= a1;
+      }
+      e[0] *= a0;
+      e[1] *= a1;
+      e[2] *= a0;
+      e[3] *= a1;
+    }
+    // 3. P as three bf16 terms, transposed into the second product's fragments
+    uint32_t bp[kPair][kPt][2];
+#pragma unroll
+    for (int y = 0; y < kPair; ++y)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float p0 = ex2(s[y][2 * x] - m0), p1 = ex2(s[y][2 * x + 1] - m1);
+        const uint32_t h = pack_bf16(p0, p1);
+        const float r0 = p0 - bf16_lo(h), r1 = p1 - bf16_hi(h);
+        const uint32_t l = pack_bf16(r0, r1);
+        const uint32_t r = pack_bf16(r0 - bf16_lo(l), r1 - bf16_hi(l));
+        if constexpr (GP == 4) {
+          bp[y][0][x] = transpose8x8(t < 2 ? h : l);
+          bp[y][1][x] = transpose8x8(t < 2 ? r : 0u);
+        } else {
+          bp[y][0][x] = transpose8x8(h);
+          bp[y][1][x] = transpose8x8(l);
+          bp[y][kPt - 1][x] = transpose8x8(r);
+        }
+      }
+    // 4. O^T += V^T . P^T.  Each tile's products of the slot are a chain of their
+    // own, added to the running sum in fp32: the tensor cores truncate what they
+    // add to, which over a long chain would leave 1e-6 of the result.
+    const int vr[4] = {v0, v1, v0 + 1, v1 + 1};
+    uint32_t la[kPair], lb[kPair], ha[kPair], hb[kPair], oa[kPair], ob[kPair];  // of rows (v0, v1), (v0 + 1, v1 + 1)
+    {
+      float te[4];
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        const uint8_t *vp = base + (2 * y + 1) * S::kPageBytes;
+        uint32_t hd[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) hd[x] = *reinterpret_cast<const uint32_t *>(vp + vr[x] * S::kRow + (n >> 1) * 4);
+        if (valid < kPair * kPage) {  // rows past the end: 0 * code + 0, whatever the bytes are
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (y * kPage + vr[x] >= valid) hd[x] = 0;
+        }
+        unpack_steps(__byte_perm(hd[0], hd[1], 0x7632), la[y], ha[y], oa[y]);
+        unpack_steps(__byte_perm(hd[2], hd[3], 0x7632), lb[y], hb[y], ob[y]);
+        const uint32_t ma = __byte_perm(hd[0], hd[1], 0x5410), mb = __byte_perm(hd[2], hd[3], 0x5410);
+#pragma unroll
+        for (int x = 0; x < kPt; ++x) {
+          if (x + y == 0)
+            mma16816_zero(te, ma, kOnes, mb, kOnes, bp[y][x][0], bp[y][x][1]);
+          else
+            mma16816(te, ma, kOnes, mb, kOnes, bp[y][x][0], bp[y][x][1]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) e[x] += te[x];
+    }
+    // codes: D = 128: lane n's channels 16n + i (word 0: rows n of tile i) and 16n + 8 + i (word 1: rows n + 8);
+    // D = 64: channels 8n + i and 8n + 4 + i, the halves of one word
+    uint32_t w[kPair][4][D / 64];
+#pragma unroll
+    for (int y = 0; y < kPair; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t *src = base + (2 * y + 1) * S::kPageBytes + vr[x] * S::kRow + kInt4Header;
+        if constexpr (D == 128) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(src + n * 8);
+          w[y][x][0] = v.x;
+          w[y][x][D / 64 - 1] = v.y;
+        } else {
+          w[y][x][0] = *reinterpret_cast<const uint32_t *>(src + n * 4);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < S::kTiles / 2; ++j) {  // byte j of a word: tiles 2j and 2j + 1
+      float t0[4], t1[4];
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        // byte a of word x of two rows, in the halves of a register
+        const uint32_t by0 = 0x4400u + 0x1111u * j, by1 = D == 128 ? by0 : by0 + 0x2222u;
+        constexpr int z = D / 64 - 1;
+        const uint32_t xa = __byte_perm(w[y][0][0], w[y][1][0], by0), xb = __byte_perm(w[y][2][0], w[y][3][0], by0);
+        const uint32_t za = __byte_perm(w[y][0][z], w[y][1][z], by1), zb = __byte_perm(w[y][2][z], w[y][3][z], by1);
+        const uint32_t a0 = fma_bf16x2(xa & 0x000f000fu, la[y], oa[y]), a1 = fma_bf16x2(za & 0x000f000fu, la[y], oa[y]);
+        const uint32_t a2 = fma_bf16x2(xb & 0x000f000fu, lb[y], ob[y]), a3 = fma_bf16x2(zb & 0x000f000fu, lb[y], ob[y]);
+        const uint32_t b0 = fma_bf16x2(xa & 0x00f000f0u, ha[y], oa[y]), b1 = fma_bf16x2(za & 0x00f000f0u, ha[y], oa[y]);
+        const uint32_t b2 = fma_bf16x2(xb & 0x00f000f0u, hb[y], ob[y]), b3 = fma_bf16x2(zb & 0x00f000f0u, hb[y], ob[y]);
+#pragma unroll
+        for (int x = 0; x < kPt; ++x) {
+          if (x + y == 0) {
+            mma16816_zero(t0, a0, a1, a2, a3, bp[y][x][0], bp[y][x][1]);
+            mma16816_zero(t1, b0, b1, b2, b3, bp[y][x][0], bp[y][x][1]);
+          } else {
+            mma16816(t0, a0, a1, a2, a3, bp[y][x][0], bp[y][x][1]);
+            mma16816(t1, b0, b1, b2, b3, bp[y][x][0], bp[y][x][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        o[2 * j][x] += t0[x];
+        o[2 * j + 1][x] += t1[x];
+      }
+    }
+    __syncwarp();  // every lane has read the slot
+    if (k + kStages < n_my) issue_pair(k + kStages);
   }
+  if (k < n_my) {  // a wait ran out: let this warp's copies land (bounded), then leave through the epilogue
+    *abort_flag = 1;
+    if (lane == 0)
+      for (int j = k; j < min(n_my, k + kStages); ++j)
+        mbar_wait(&full[warp][j % kStages], (uint32_t)((j / kStages) & 1), abort_flag, p.status, false);
+  }
+
+  // the low terms of P sit two lanes on (GP = 4)
+#pragma unroll
+  for (int i = 0; i < S::kTiles; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if constexpr (GP == 4) o[i][x] += __shfl_xor_sync(0xffffffffu, o[i][x], 2);
+  if constexpr (GP == 4)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) e[x] += __shfl_xor_sync(0xffffffffu, e[x], 2);
+  __syncthreads();  // every warp is past its loop: the page slots are free
+  float *red = reinterpret_cast<float *>(smem);  // [kWarps][G][D]
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int g = 2 * t + x;
+    if (g >= G || (GP == 4 && t >= 2)) continue;
+    float *dst = red + (warp * G + g) * D + n * (D / 8);
+#pragma unroll
+    for (int i = 0; i < S::kTiles; ++i) {
+      dst[i] = fmaf(o[i][x], 0x1p64f, e[x]);
+      dst[S::kTiles + i] = fmaf(o[i][2 + x], 0x1p64f, e[x]);
+    }
+    if (n == 0) {
+      m_s[warp * G + g] = x ? m1 : m0;
+      l_s[warp * G + g] = e[2 + x];
+    }
+  }
+  __syncthreads();
+  attn_finish<D, kWarps, kThreads>(p, u, G, red, m_s, l_s, mg, ACC ? scores : nullptr);
+}
+
+template <int D, int GP, bool ACC>
+cudaError_t launch4(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
+  auto kernel = decode_attention4_kernel<D, GP, ACC>;
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + Shape4<D>::kRing,
+                             ACC ? (size_t)kPage * G * 4 : 0, kThreads, s);
 }
 
 }  // namespace
 
-bool decode_attention4_supported(int dtype, int head_dim, int G) {
-  return (dtype == KVC_BF16 || dtype == KVC_F32 || dtype == KVC_INT4) && (head_dim == 64 || head_dim == 128) &&
-         (G == 1 || G == 2 || G == 4 || G == 8);
+// Picks the cluster size and launches a cluster-form attention kernel with
+// arguments (DecodeAttnParams, int G).
+//   base_smem: shared memory without the scores; page_smem: bytes of scores
+//   per page (0 without weights); np_max: most pages of a request.
+// The cluster is the smallest power of two up to 16 whose CTAs can hold their
+// rows' scores in shared memory and of which at least two waves fill the GPU,
+// as long as every warp keeps two pages: many units need no split, a few long
+// requests take all the SMs.
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
+                                size_t page_smem, int threads, cudaStream_t s) {
+  constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // less the static shared memory
+  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
+  if (units <= 0) return cudaSuccess;
+  auto smem_of = [&](int cs) { return base_smem + page_smem * ((size_t)(np_max + cs - 1) / cs); };
+  int cs = 1;
+  while (cs < 16 && (smem_of(cs) > kMaxSmem || (units * cs < 4LL * sms && np_max > cs * 2 * (threads / 32)))) cs *= 2;
+  const size_t smem = smem_of(cs);
+  if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  if (cs > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
+  p.nsplit = cs;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cs;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  void *args[] = {&p, &G};
+  return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int dtype, int G, int row_bytes,
+cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
                                      cudaStream_t s) {
-  const int units = p.layer_count * p.R * p.hkv;
-  auto kernel = attend_kernel<KVC_F32, 128>;
-  if (dtype == KVC_F32) kernel = head_dim == 128 ? attend_kernel<KVC_F32, 128> : attend_kernel<KVC_F32, 64>;
-  if (dtype == KVC_BF16) kernel = head_dim == 128 ? attend_kernel<KVC_BF16, 128> : attend_kernel<KVC_BF16, 64>;
-  if (dtype == KVC_INT4) kernel = head_dim == 128 ? attend_kernel<KVC_INT4, 128> : attend_kernel<KVC_INT4, 64>;
-  kernel<<<units, kThreads, 0, s>>>(p, G, row_bytes);
-  return cudaGetLastError();
+  const bool acc = p.weights != nullptr;
+  if (head_dim == 128) {
+    if (G <= 4) return acc ? launch4<128, 4, true>(p, G, np_max, sms, s) : launch4<128, 4, false>(p, G, np_max, sms, s);
+    return acc ? launch4<128, 8, true>(p, G, np_max, sms, s) : launch4<128, 8, false>(p, G, np_max, sms, s);
+  }
+  if (G <= 4) return acc ? launch4<64, 4, true>(p, G, np_max, sms, s) : launch4<64, 4, false>(p, G, np_max, sms, s);
+  return acc ? launch4<64, 8, true>(p, G, np_max, sms, s) : launch4<64, 8, false>(p, G, np_max, sms, s);
 }
 
 }  // namespace kvc

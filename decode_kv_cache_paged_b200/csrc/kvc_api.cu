@@ -903,8 +903,7 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   if (((uintptr_t)q % ctx->es) || ((uintptr_t)out & 3) || ((uintptr_t)lse & 3))
     return fail(ctx, KVC_ERR_INVALID_ARG, "q, out or lse misaligned");
   const int G = ctx->G;
-  const bool plain = c.dtype != KVC_INT4 && !o.accumulate;  // the step without a 4-bit cache or weights
-  if (!(plain ? decode_attention_supported(c.dtype, c.head_dim, G) : decode_attention4_supported(c.dtype, c.head_dim, G)))
+  if (!decode_attention_supported(c.dtype, c.head_dim, G))
     return fail(ctx, KVC_ERR_UNSUPPORTED,
                 "decode attention needs head_dim 64 or 128 and 1, 2, 4 or 8 query heads per KV head");
   const int R = c.num_requests;
@@ -947,8 +946,17 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   p.decay = o.decay;
   if (ms_out) KVC_CUDA(ctx, cudaEventRecord(ctx->ev[0], ctx->stream));
   int launches = 0;
-  cudaError_t e = plain ? launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream)
-                        : launch_decode_attention4(p, c.head_dim, c.dtype, G, ctx->row_bytes, ctx->stream);
+  cudaError_t e;
+  if (c.dtype != KVC_INT4 && !o.accumulate) {
+    e = launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream);
+  } else {
+    // a captured step may be replayed over a longer cache than today's
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
+    const int pages = cap == cudaStreamCaptureStatusNone ? np_max : ctx->maxp;
+    e = c.dtype == KVC_INT4 ? launch_decode_attention4(p, c.head_dim, G, pages, ctx->num_sms, ctx->stream)
+                            : launch_decode_attention_acc(p, c.head_dim, c.dtype, G, pages, ctx->num_sms, ctx->stream);
+  }
   if (e != cudaSuccess) return cuda_fail(ctx, e, "decode_attention");
   if (ms_out) {
     KVC_CUDA(ctx, cudaEventRecord(ctx->ev[1], ctx->stream));

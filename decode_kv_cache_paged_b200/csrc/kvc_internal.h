@@ -65,7 +65,8 @@ struct DecodeAttnParams {
   float *part_ml;              // [layer_count][R][Hq][nsplit][2] (max in base 2, sum)
   int32_t *status;
   int64_t num_pages;
-  int32_t bt_stride, layer_begin, layer_count, R, hkv, hq, nsplit, pages_per_split;
+  int32_t bt_stride, layer_begin, layer_count, R, hkv, hq;
+  int32_t nsplit, pages_per_split;  // CTAs of a unit (cluster forms: of its cluster); pages of each (not used there)
   float qscale;                // scale * log2(e)
   float *weights;              // accumulated attention weights, indexed like the position map, or null
   float decay;                 // weights <- decay * weights + this step's
@@ -132,9 +133,15 @@ cudaError_t launch_wait_timeout_probe(int32_t *status, uint32_t limit_ms, cudaSt
 bool decode_attention_supported(int dtype, int head_dim, int G);
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s);
-bool decode_attention4_supported(int dtype, int head_dim, int G);
-cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int dtype, int G, int row_bytes,
+// The cluster forms (attn_cluster.cuh): over the 4-bit cache, and accumulating
+// weights over the other caches.  np_max: most pages a request may have when
+// the launch runs; sms: the device's SMs.
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
+                                size_t page_smem, int threads, cudaStream_t s);
+cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
                                      cudaStream_t s);
+cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, int np_max, int sms,
+                                        cudaStream_t s);
 cudaError_t launch_select_compact(const SelectCompactParams &p, int mode, int n_seg_req,
                                   int max_n, int max_m, cudaStream_t s);
 cudaError_t launch_beacon_update(const BeaconUpdateParams &p, int n_req, cudaStream_t s);

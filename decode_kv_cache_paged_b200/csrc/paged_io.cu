@@ -64,7 +64,7 @@ __global__ void append_kv_kernel(const uint8_t *__restrict__ k_src, const uint8_
 // bf16) each, so a group of D/4 channels is 4 lanes (D = 128) or 2 (D = 64):
 // its smallest and largest value come from one or two shuffles, and the lanes
 // of a row write its codes 4 bytes apiece, side by side.
-template <int D>
+template <int D, bool IS_V>
 __device__ __forceinline__ void int4_code_chunk(uint4 x4, uint8_t *row, int v, unsigned lanes) {
   constexpr int kLanes = D / 8 / kInt4Groups;  // lanes of one group
   const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
@@ -88,17 +88,21 @@ __device__ __forceinline__ void int4_code_chunk(uint4 x4, uint8_t *row, int v, u
     bad += __shfl_xor_sync(lanes, bad, m);
   }
   float s = int4_step(lo, hi) + bad;
-  if (isnan(s)) lo = s;
   uint32_t codes = 0;
   if (s > 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) codes |= (uint32_t)__float2int_rn(__fdiv_rn(x[i] - lo, s)) << (4 * i);
   }
-  if (v % kLanes == 0) {
-    const uint32_t h = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
-    *reinterpret_cast<uint32_t *>(row + (v / kLanes) * 4) = h;
+  if (v % kLanes == 0) *reinterpret_cast<uint32_t *>(row + (v / kLanes) * 4) = int4_word<IS_V>(s, lo);
+  uint8_t *dst = row + kInt4Header;
+  if constexpr (IS_V) {
+    reinterpret_cast<uint32_t *>(dst)[v] = codes;
+  } else if constexpr (D == 128) {
+    reinterpret_cast<uint32_t *>(dst)[int4_k_word(v)] = codes;
+  } else {
+    reinterpret_cast<uint16_t *>(dst)[int4_k_half(2 * v)] = (uint16_t)codes;
+    reinterpret_cast<uint16_t *>(dst)[int4_k_half(2 * v + 1)] = (uint16_t)(codes >> 16);
   }
-  *reinterpret_cast<uint32_t *>(row + kInt4Header + v * 4) = codes;
 }
 
 template <int D>
@@ -126,8 +130,8 @@ __global__ void append_kv4_kernel(const uint4 *__restrict__ k_src, const uint4 *
   const int page = block_table[(int64_t)d.x * bt_stride + (slot >> 4)];
   const int64_t row = (((int64_t)l * num_pages + page) * hkv + h) * kPage + (slot & (kPage - 1));
   const uint4 kx = k_src[g], vx = v_src[g];
-  int4_code_chunk<D>(kx, k_pool + row * int4_row_bytes(D), v, lanes);
-  int4_code_chunk<D>(vx, v_pool + row * int4_row_bytes(D), v, lanes);
+  int4_code_chunk<D, false>(kx, k_pool + row * int4_row_bytes(D), v, lanes);
+  int4_code_chunk<D, true>(vx, v_pool + row * int4_row_bytes(D), v, lanes);
   if (v == 0) {
     pos_map[row] = d.z + t;
     if (weights) weights[row] = 0.f;
@@ -188,15 +192,24 @@ __global__ void gather_dense_kernel(const uint8_t *__restrict__ k_pool, const ui
   if (pos_out && v == 0) pos_out[g / vpr] = pos;
 }
 
-// the values of 8 codes of group (v * 8) / (D / 4): one lane's share of a row
-template <int D>
+// the values of channels 8 v .. 8 v + 7: one lane's share of a row
+template <int D, bool IS_V>
 __device__ __forceinline__ void int4_values(const uint8_t *row, int v, float4 &a, float4 &b) {
   const uint32_t h = *reinterpret_cast<const uint32_t *>(row + (v * 8 / (D / kInt4Groups)) * 4);
-  const uint32_t c = *reinterpret_cast<const uint32_t *>(row + kInt4Header + v * 4);
-  const float s = __uint_as_float(h << 16), lo = __uint_as_float(h & 0xffff0000u);
-  float x[8];
+  const uint8_t *src = row + kInt4Header;
+  uint32_t c;
+  if constexpr (IS_V) {
+    c = reinterpret_cast<const uint32_t *>(src)[v];
+  } else if constexpr (D == 128) {
+    c = reinterpret_cast<const uint32_t *>(src)[int4_k_word(v)];
+  } else {
+    c = reinterpret_cast<const uint16_t *>(src)[int4_k_half(2 * v)] |
+        (uint32_t)reinterpret_cast<const uint16_t *>(src)[int4_k_half(2 * v + 1)] << 16;
+  }
+  float s, zs, mid, x[8];
+  int4_unword(h, s, zs, mid);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((c >> (4 * i)) & 15u), s, lo);
+  for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((c >> (4 * i)) & 15u), s, -zs) + mid;  // the fma is exact
   a = make_float4(x[0], x[1], x[2], x[3]);
   b = make_float4(x[4], x[5], x[6], x[7]);
 }
@@ -226,8 +239,8 @@ __global__ void gather_dense4_kernel(const uint8_t *__restrict__ k_pool, const u
   if (slot < lengths[r]) {
     const int page = block_table[(int64_t)r * bt_stride + (slot >> 4)];
     const int64_t row = (((int64_t)layer * num_pages + page) * hkv + h) * kPage + (slot & (kPage - 1));
-    if (k_out) int4_values<D>(k_pool + row * int4_row_bytes(D), v, k0, k1);
-    if (v_out) int4_values<D>(v_pool + row * int4_row_bytes(D), v, v0, v1);
+    if (k_out) int4_values<D, false>(k_pool + row * int4_row_bytes(D), v, k0, k1);
+    if (v_out) int4_values<D, true>(v_pool + row * int4_row_bytes(D), v, v0, v1);
     pos = pos_map[row];
   }
   if (k_out) {

@@ -87,14 +87,21 @@ typedef enum {
  * row of head_dim channels (64 or 128) is kept as four groups of head_dim/4
  * channels.  With lo and hi a group's smallest and largest value,
  *     s     = (hi - lo) / 15 rounded up to four significant bits
- *             (0 where (hi - lo) / 15 < 2^-100),
+ *             (0 where (hi - lo) / 15 < 2^-56),
  *     code  = rint((x - lo) / s), ties to even (0 where s = 0),
  *     value = lo + s * code,
- * so a value is off by at most s / 2; a group that holds an infinity or a
- * NaN, or whose (hi - lo) / 15 reaches 2^100, stands for NaN.  Row bytes: the
- * (s, lo) bf16 pairs of groups 0..3, then head_dim/2 bytes of codes, the
- * lower channel in a byte's low half: head_dim/2 + 16 in all (80 at head_dim
- * 128, against 256 in bf16).  The random and the attention selectors, both
+ * so a value is off by at most s / 2 (differences and quotients rounded to
+ * fp32); a group that holds an infinity or a NaN, or whose (hi - lo) / 15
+ * reaches 2^56, stands for NaN.  Row bytes: one 4-byte word for each group,
+ * then head_dim/2 bytes of codes: head_dim/2 + 16 in all.  A word's high half
+ * is s as bf16 with its four lowest bits replaced by z, its low half mid as
+ * bf16, and value = mid + s * (code - z).  K rows: z = 0, mid = lo; V rows: z =
+ * min(15, rint(-lo / s)) where 0 < -lo / 2^e < 32 with 2^e the power of two at
+ * or below s, else 0, and mid = lo + z * s (exact); a NaN group has s = z = 0
+ * and mid = NaN.  The codes of a V row are in channel order, the lower channel
+ * in a byte's low half; those of a K row come in units of head_dim/16
+ * channels, of which unit t of group g is unit 4 t + g.  (80 bytes a row at
+ * head_dim 128, against 256 in bf16).  The random and the attention selectors, both
  * compactions and decode attention work on it; the beacon selectors do not
  * (num_beacons must be 0). */
 typedef enum { KVC_BF16 = 0, KVC_F32 = 1, KVC_INT4 = 2 } kvc_dtype;

@@ -5,21 +5,37 @@ import numpy as np
 
 def code_rows(x):
     """(step, lo, codes) of rows x [..., d] float64 (each a bf16 value): step and lo [..., 4], codes [..., 4, d/4].
-    A group that is not finite, or too wide, has NaN step and lo and codes 0."""
+    A group that is not finite, or too wide, has NaN step and lo and codes 0.  Differences and quotients are rounded to
+    fp32, as the definition says (numpy's float32 operations are correctly rounded)."""
     x = np.asarray(x, np.float64)
     g = x.reshape(*x.shape[:-1], 4, x.shape[-1] // 4)
     fine = np.isfinite(g).all(-1)
-    safe = np.where(fine[..., None], g, 0.0)
+    safe = np.where(fine[..., None], g, 0.0).astype(np.float32)
     lo = safe.min(-1)
-    r = (safe.max(-1) - lo) / 15.0
+    with np.errstate(over="ignore"):
+        r = ((safe.max(-1) - lo) / np.float32(15.0)).astype(np.float64)
     m, e = np.frexp(r)
-    step = np.where(r >= 2.0 ** -100, np.ldexp(np.ceil(m * 16) / 16, e), 0.0)
-    codes = np.zeros_like(safe)
-    on = step > 0
-    codes[on] = np.rint((safe[on] - lo[on][..., None]) / step[on][..., None])
+    step = np.where(r >= 2.0 ** -56, np.ldexp(np.ceil(m * 16) / 16, e), 0.0)
+    bad = ~fine | (r >= 2.0 ** 56)
+    codes = np.zeros(g.shape)
+    on = (step > 0) & ~bad
+    codes[on] = np.rint((safe[on] - lo[on][..., None]) / step[on][..., None].astype(np.float32))
     assert codes.min(initial=0) >= 0 and codes.max(initial=0) <= 15
-    bad = ~fine | (r >= 2.0 ** 100)
-    return np.where(bad, np.nan, step), np.where(bad, np.nan, lo), np.where(bad[..., None], 0.0, codes)
+    return np.where(bad, np.nan, step), np.where(bad, np.nan, lo.astype(np.float64)), np.where(bad[..., None], 0.0, codes)
+
+
+def centres(step, lo):
+    """(z, mid) of a V row's finite groups: z = min(15, rint(-lo / step)) where 0 < -lo / 2^e < 32, mid = lo + z * step."""
+    unit = np.where(step > 0, 2.0 ** (np.frexp(step)[1] - 1), 1.0)
+    on = (step > 0) & (-lo / unit > 0) & (-lo / unit < 32)
+    z = np.where(on, np.minimum(np.rint(np.float32(-lo) / np.where(step > 0, step, 1).astype(np.float32)), 15), 0.0)
+    return z, lo + z * step
+
+
+def k_order(codes):
+    """Codes [..., d] of K rows in the order of the row's bytes: unit t of group g is unit 4 t + g."""
+    u = codes.reshape(*codes.shape[:-1], 4, 4, codes.shape[-1] // 16)  # group, unit, channel
+    return u.swapaxes(-3, -2).reshape(codes.shape)
 
 
 def row_values(x):

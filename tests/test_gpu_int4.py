@@ -48,10 +48,10 @@ def rows(n, layers, H, d, seed, kind="normal", dtype=torch.bfloat16):
     elif kind == "zero":
         x = torch.zeros_like(x)
     elif kind == "wide":
-        x = x * 2.0 ** torch.randint(-60, 60, x.shape[:-1] + (1,), generator=g, device="cuda")
+        x = x * 2.0 ** torch.randint(-40, 40, x.shape[:-1] + (1,), generator=g, device="cuda")
     elif kind == "edge":  # ranges around the smallest step and the largest one
         e = torch.randint(0, 4, x.shape[:-1] + (1,), generator=g, device="cuda")
-        x = torch.where(e == 0, x * 2.0 ** -98, torch.where(e == 1, x * 2.0 ** -115, torch.where(e == 2, x * 2.0 ** 102, x * 2.0 ** 108)))
+        x = torch.where(e == 0, x * 2.0 ** -54, torch.where(e == 1, x * 2.0 ** -70, torch.where(e == 2, x * 2.0 ** 58, x * 2.0 ** 90)))
     elif kind == "broken":
         bad = torch.randint(0, 200, x.shape, generator=g, device="cuda")
         x = torch.where(bad == 0, float("inf"), torch.where(bad == 1, float("-inf"), torch.where(bad == 2, float("nan"), x)))
@@ -98,19 +98,24 @@ def test_values_are_the_definitions(d, kind):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_row_bytes_are_the_documented_ones(d):
+@pytest.mark.parametrize("kind", ["hot", "ties", "offset", "wide", "zero"])
+def test_row_bytes_are_the_documented_ones(d, kind):
     ctx = make([20], H=2, d=d)
-    (k, v), = fill(ctx, [20], seed=8)
+    (k, v), = fill(ctx, [20], seed=8, kind=kind)
     assert ctx.view().row_bytes == d // 2 + 16 == ctx.k_pool.shape[-1]
     bt = ctx.state_tensors()["block_table"].cpu()
-    for pool, x in ((ctx.k_pool, k), (ctx.v_pool, v)):
+    for pool, x, is_v in ((ctx.k_pool, k, False), (ctx.v_pool, v, True)):
         step, lo, codes = rows4.code_rows(np64(x[0]).transpose(1, 0, 2))
+        z, mid = rows4.centres(step, lo) if is_v else (np.zeros_like(lo), lo)
         for j in (0, 15, 16, 19):
             raw = pool[0, int(bt[0, j // 16]), :, j % 16].cpu().numpy()  # [H, row bytes]
             head = raw[:, :16].copy().view(np.uint32)
-            assert np.array_equal((head << 16).view(np.float32), step[:, j].astype(np.float32))
-            assert np.array_equal((head & 0xFFFF0000).view(np.float32), lo[:, j].astype(np.float32))
+            assert np.array_equal((head & 0xFFF00000).view(np.float32), step[:, j].astype(np.float32))
+            assert np.array_equal(head >> 16 & 15, z[:, j].astype(np.uint32))
+            have = (head << 16).view(np.float32).astype(np.float64)
+            assert np.array_equal(have, mid[:, j])  # exactly: mid needs no rounding
             c = codes[:, j].reshape(2, d).astype(np.uint8)
+            c = c if is_v else rows4.k_order(c)
             assert np.array_equal(raw[:, 16:], c[:, 0::2] | (c[:, 1::2] << 4))
     ctx.close()
 
