@@ -18,11 +18,6 @@
 namespace kvc {
 namespace {
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -35,6 +30,12 @@ __device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ float attn_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct AttnUnit {
   int rank, cs;              // this CTA in its cluster, and the cluster's size
   int lc, l, r, h;           // layer (in the call, in the cache), request, KV head
@@ -45,7 +46,7 @@ struct AttnUnit {
 __device__ __forceinline__ AttnUnit attn_unit(const DecodeAttnParams &p) {
   AttnUnit u;
   u.cs = p.nsplit;
-  u.rank = u.cs > 1 ? (int)cluster_rank() : 0;
+  u.rank = blockIdx.x % u.cs;  // clusters are runs of u.cs blocks
   const int unit = blockIdx.x / u.cs;
   u.h = unit % p.hkv;
   u.r = (unit / p.hkv) % p.R;
@@ -61,97 +62,161 @@ __device__ __forceinline__ AttnUnit attn_unit(const DecodeAttnParams &p) {
 }
 
 // Shared scratch of the epilogue.
+template <int W>
 struct AttnMerge {
-  float m[8], l[8];                // this CTA's running maximum (base 2) and sum per head
-  float all_m[16][8], all_l[16][8];  // every CTA's
-  float fac[16][8];                // exp2(m of the CTA - m of the unit) / sum of the unit
-  float lse2[8];                   // the unit's log2-sum-exp2
+  float m[8], l[8];                    // this CTA's running maximum (base 2) and sum per head
+  float part[W][8];                    // the warps' factors
+  float all_m[16][8], all_l[16][8];    // every CTA's
+  float fac[16][8];                    // exp2(m of the CTA - m of the unit) / sum of the unit
+  float lse2[8];                       // the unit's log2-sum-exp2
 };
+
+// Adds the weights of this CTA's rows from their base-2 scores [page][G][16].
+// A thread takes four rows of a page at a time (a page's 16 weights are one
+// 64-byte run) and starts the reads of kBatch such quads before the first is
+// used: one after the other the loop waits for memory once per quad, which
+// cost a third of the step at 2048 rows.
+template <int NT, int G>
+__device__ __forceinline__ void attn_add_weights(const DecodeAttnParams &p, const AttnUnit &u,
+                                                 const float (&lse2)[8], const float *scores) {
+  constexpr int kBatch = 4;
+  const int rows = min(u.len, u.pg1 * kPage) - u.pg0 * kPage;
+  float *w0 = p.weights + ((int64_t)u.l * p.num_pages * p.hkv + u.h) * kPage;
+  const int64_t page_stride = (int64_t)p.hkv * kPage;
+  for (int j0 = threadIdx.x * 4; j0 < rows; j0 += 4 * NT * kBatch) {
+    float4 w[kBatch];
+    float *at[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int j = j0 + b * 4 * NT;
+      if (j < rows) at[b] = w0 + u.bt[u.pg0 + j / kPage] * page_stride + j % kPage;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (j0 + b * 4 * NT < rows) w[b] = *reinterpret_cast<const float4 *>(at[b]);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int j = j0 + b * 4 * NT;
+      if (j >= rows) continue;
+      const float *sc = scores + (j / kPage) * (kPage * G) + j % kPage;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4 v = *reinterpret_cast<const float4 *>(sc + g * kPage);
+        a.x += attn_ex2(v.x - lse2[g]);
+        a.y += attn_ex2(v.y - lse2[g]);
+        a.z += attn_ex2(v.z - lse2[g]);
+        a.w += attn_ex2(v.w - lse2[g]);
+      }
+      a = make_float4(fmaf(p.decay, w[b].x, a.x), fmaf(p.decay, w[b].y, a.y), fmaf(p.decay, w[b].z, a.z),
+                      fmaf(p.decay, w[b].w, a.w));
+      if (j + 4 <= rows) {
+        *reinterpret_cast<float4 *>(at[b]) = a;
+      } else {  // the last rows: what lies past them stays
+        at[b][0] = a.x;
+        if (j + 1 < rows) at[b][1] = a.y;
+        if (j + 2 < rows) at[b][2] = a.z;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void attn_write_lse(const DecodeAttnParams &p, int64_t head, float lse2) {
+  if (p.lse) p.lse[head] = lse2 * 0.6931471805599453f;
+  if (p.lse2) p.lse2[head] = lse2;
+}
 
 // Merges the warps' and then the CTAs' states and writes the outputs.
 //   red:  [W][G][D] the warps' sums, m_s, l_s: [W][G] their maxima and sums
 //         (a warp without rows has l = 0); the caller has synchronised.
-//   scores: [rows of this CTA][G] base-2 scores, or null (no weights).
+//   scores: [pages of this CTA][G][16] base-2 scores, or null (no weights).
 // Every thread of the CTA calls it.
 template <int D, int W, int NT>
 __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const AttnUnit &u, int G, float *red,
-                                            const float *m_s, const float *l_s, AttnMerge &mg, const float *scores) {
+                                            const float *m_s, const float *l_s, AttnMerge<W> &mg, const float *scores) {
   const int tid = threadIdx.x;
-  for (int i = tid; i < G * D; i += NT) {
-    const int g = i / D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w * G + g]);
-    float o = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float lw = l_s[w * G + g];
-      if (lw == 0.f) continue;
-      const float sc = exp2f(m_s[w * G + g] - M);
-      o = fmaf(red[w * G * D + i], sc, o);
-      l = fmaf(lw, sc, l);
-    }
-    red[i] = o;
-    if (i % D == 0) {
-      mg.m[g] = M;
-      mg.l[g] = l;
-    }
-  }
-  if (u.cs > 1)
-    cluster_sync_all();
-  else
-    __syncthreads();
   const int64_t head0 = ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
-  for (int i = tid; i < u.cs * 8; i += NT) {
-    const int c = i >> 3, g = i & 7;
-    if (g < G) {
-      mg.all_m[c][g] = u.cs > 1 ? ld_cluster(&mg.m[g], c) : mg.m[g];
-      mg.all_l[c][g] = u.cs > 1 ? ld_cluster(&mg.l[g], c) : mg.l[g];
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < u.cs * 8; i += NT) {
-    const int c = i >> 3, g = i & 7;
+  // the warps' factors; alone in its cluster a CTA divides by the sum at once
+  for (int i = tid; i < W * 8; i += NT) {
+    const int w = i >> 3, g = i & 7;
     if (g >= G) continue;
     float M = -INFINITY, L = 0.f;
-    for (int x = 0; x < u.cs; ++x) M = fmaxf(M, mg.all_m[x][g]);
-    for (int x = 0; x < u.cs; ++x)
-      if (mg.all_l[x][g] != 0.f) L = fmaf(mg.all_l[x][g], exp2f(mg.all_m[x][g] - M), L);
-    mg.fac[c][g] = mg.all_l[c][g] != 0.f ? exp2f(mg.all_m[c][g] - M) / L : 0.f;
-    if (c == 0) {
-      const float lse2 = M + log2f(L);
-      mg.lse2[g] = lse2;
-      if (u.rank == 0 && p.lse) p.lse[head0 + g] = u.len > 0 ? lse2 * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+    for (int x = 0; x < W; ++x) M = fmaxf(M, m_s[x * G + g]);
+#pragma unroll
+    for (int x = 0; x < W; ++x)
+      if (l_s[x * G + g] != 0.f) L = fmaf(l_s[x * G + g], attn_ex2(m_s[x * G + g] - M), L);
+    const float f = l_s[w * G + g] != 0.f ? attn_ex2(m_s[w * G + g] - M) : 0.f;
+    mg.part[w][g] = u.cs > 1 || f == 0.f ? f : f / L;
+    if (w == 0) {
+      mg.m[g] = M;
+      mg.l[g] = L;
+      if (u.cs == 1) {
+        const float lse2 = M + log2f(L);
+        mg.lse2[g] = lse2;
+        attn_write_lse(p, head0 + g, u.len > 0 ? lse2 : -INFINITY);
+      }
     }
   }
   __syncthreads();
-  // outputs: each CTA of the cluster writes its share of the G * D values
-  const int share = (G * D + u.cs - 1) / u.cs;
-  for (int i = u.rank * share + tid; i < min(G * D, (u.rank + 1) * share); i += NT) {
+  for (int i = tid; i < G * D; i += NT) {
     float o = 0.f;
-    if (u.cs > 1) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = mg.part[w][i / D];
+      if (f != 0.f) o = fmaf(red[w * G * D + i], f, o);
+    }
+    if (u.cs > 1)
+      red[i] = o;
+    else
+      p.out[head0 * D + i] = o;
+  }
+  if (u.cs > 1) {
+    cluster_sync_all();
+    for (int i = tid; i < u.cs * 8; i += NT) {
+      const int c = i >> 3, g = i & 7;
+      if (g < G) {
+        mg.all_m[c][g] = ld_cluster(&mg.m[g], c);
+        mg.all_l[c][g] = ld_cluster(&mg.l[g], c);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < u.cs * 8; i += NT) {
+      const int c = i >> 3, g = i & 7;
+      if (g >= G) continue;
+      float M = -INFINITY, L = 0.f;
+      for (int x = 0; x < u.cs; ++x) M = fmaxf(M, mg.all_m[x][g]);
+      for (int x = 0; x < u.cs; ++x)
+        if (mg.all_l[x][g] != 0.f) L = fmaf(mg.all_l[x][g], attn_ex2(mg.all_m[x][g] - M), L);
+      mg.fac[c][g] = mg.all_l[c][g] != 0.f ? attn_ex2(mg.all_m[c][g] - M) / L : 0.f;
+      if (c == 0) {
+        const float lse2 = M + log2f(L);
+        mg.lse2[g] = lse2;
+        if (u.rank == 0) attn_write_lse(p, head0 + g, u.len > 0 ? lse2 : -INFINITY);
+      }
+    }
+    __syncthreads();
+    // outputs: each CTA of the cluster writes its share of the G * D values
+    const int share = (G * D + u.cs - 1) / u.cs;
+    for (int i = u.rank * share + tid; i < min(G * D, (u.rank + 1) * share); i += NT) {
+      float o = 0.f;
 #pragma unroll 4
       for (int x = 0; x < u.cs; ++x) {
         const float f = mg.fac[x][i / D], v = ld_cluster(&red[i], x);
         if (f != 0.f) o = fmaf(v, f, o);
       }
-    } else {
-      o = red[i] * mg.fac[0][i / D];
+      p.out[head0 * D + i] = o;
     }
-    p.out[head0 * D + i] = u.len > 0 ? o : 0.f;
   }
   if (scores) {
     float lse2[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) lse2[x] = x < G ? mg.lse2[x] : 0.f;
-    const int rows = min(u.len, u.pg1 * kPage) - u.pg0 * kPage;
-    for (int j = tid; j < rows; j += NT) {
-      float w = 0.f;
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x < G) w += exp2f(scores[j * G + x] - lse2[x]);
-      const int64_t at = (((int64_t)u.l * p.num_pages + u.bt[u.pg0 + j / kPage]) * p.hkv + u.h) * kPage + j % kPage;
-      p.weights[at] = fmaf(p.decay, p.weights[at], w);
+    switch (G) {
+      case 1: attn_add_weights<NT, 1>(p, u, lse2, scores); break;
+      case 2: attn_add_weights<NT, 2>(p, u, lse2, scores); break;
+      case 4: attn_add_weights<NT, 4>(p, u, lse2, scores); break;
+      default: attn_add_weights<NT, 8>(p, u, lse2, scores);
     }
   }
   if (u.cs > 1) cluster_sync_all();  // the others may still read this CTA's shared memory

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   __shared__ __align__(8) uint64_t full[W][NS];
   __shared__ int abort_flag_s;
   volatile int *abort_flag = &abort_flag_s;
-  [[maybe_unused]] float *scores = reinterpret_cast<float *>(smem + S::kSmem - 128);  // [rows of this CTA][G] (ACC)
+  [[maybe_unused]] float *scores = reinterpret_cast<float *>(smem + S::kSmem - 128);  // [pages of this CTA][G][16] (ACC)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   AttnUnit un{};
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
       if (writer) {
 #pragma unroll
         for (int b = 0; b < S::kBatches; ++b) {
-          float *dst = scores + ((warp + k * W) * kPage + grp * S::kRowsPerGroup + b * S::kRb + e0 / G) * G + g0;
+          float *dst = scores + ((warp + k * W) * G + g0) * kPage + grp * S::kRowsPerGroup + b * S::kRb + e0 / G;
 #pragma unroll
-          for (int kk = 0; kk < KEEP; ++kk) dst[kk] = sv[b][kk];
+          for (int kk = 0; kk < KEEP; ++kk) dst[kk * kPage] = sv[b][kk];
         }
       }
     }
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   }
   __syncthreads();
   if constexpr (ACC) {
-    __shared__ AttnMerge mg;
+    __shared__ AttnMerge<W> mg;
     attn_finish<D, W, kThreads>(p, un, G, red, &m_s[0][0], &l_s[0][0], mg, scores);
     return;
   }
@@ -515,7 +515,7 @@ template <typename T, int D, int G>
 cudaError_t launch_acc(DecodeAttnParams p, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention_kernel<T, D, G, true>;
   return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, AttnShape<T, D, G>::kSmem,
-                             (size_t)kPage * G * 4, kThreads, s);
+                             (size_t)kPage * G * 4, kThreads, true, s);
 }
 
 template <typename T, int D>

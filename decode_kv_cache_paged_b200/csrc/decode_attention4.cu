@@ -58,30 +58,15 @@
 namespace kvc {
 namespace {
 
-#ifndef KVC_ATTN4_WARPS
-#define KVC_ATTN4_WARPS 4
-#endif
-constexpr int kWarps = KVC_ATTN4_WARPS;
-constexpr int kThreads = 32 * kWarps;
-
-#ifndef KVC_ATTN4_STAGES
-#define KVC_ATTN4_STAGES 2
-#endif
-constexpr int kStages = KVC_ATTN4_STAGES;  // slots per warp
-#ifndef KVC_ATTN4_PAIR
-#define KVC_ATTN4_PAIR 2
-#endif
-constexpr int kPair = KVC_ATTN4_PAIR;      // pages per slot
-#ifndef KVC_ATTN4_MINB
-#define KVC_ATTN4_MINB 4
-#endif
+constexpr int kStages = 2;  // slots per warp
+constexpr size_t kSmemHalf = 111 * 1024;  // dynamic shared memory with which two CTAs fit an SM
+constexpr int kPair = 2;    // pages per slot
 
 template <int D>
 struct Shape4 {
   static constexpr int kRow = int4_row_bytes(D);
-  static constexpr int kPageBytes = kPage * kRow;     // K (or V) of one page
+  static constexpr int kPageBytes = kPage * kRow;       // K (or V) of one page
   static constexpr int kSlot = kPair * 2 * kPageBytes;  // K, V of the first page, K, V of the second
-  static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and K row
   static constexpr int kTiles = D / 16;  // products per page on the V side
 };
@@ -146,12 +131,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // s * 2^69, s * 2^65 and -z s / 2^64 of a pair of V rows, from their words' high halves
 __device__ __forceinline__ void unpack_steps(uint32_t r, uint32_t &s_lo, uint32_t &s_hi, uint32_t &off) {
   const uint32_t s2 = r & 0xfff0fff0u;
@@ -162,16 +141,25 @@ __device__ __forceinline__ void unpack_steps(uint32_t r, uint32_t &s_lo, uint32_
 constexpr uint32_t kOnes = 0x3f803f80u;
 constexpr float kLazy = 8.f;  // a score may exceed the running maximum by this much (base 2)
 
+// What a launch does: the step; the step with the weights added from scores
+// kept in shared memory; the weights alone, from the keys and the step's
+// log-sum-exp (p.lse2), for rows too many to keep the scores of.
+enum Mode4 { kStep, kStepWeights, kWeights };
+
 // GP: columns of the product that hold query heads, 4 (G <= 4: the second parts
-// take the other four) or 8.  ACC: keep the scores and add the weights.
-template <int D, int GP, bool ACC>
-__global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_kernel(DecodeAttnParams p, int G) {
+// take the other four) or 8.  W: warps of a CTA; 16 warps fit an SM.
+template <int D, int GP, Mode4 MODE, int W>
+__global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16) / W) decode_attention4_kernel(DecodeAttnParams p, int G) {
   using S = Shape4<D>;
+  constexpr int kWarps = W, kThreads = 32 * W;
+  constexpr bool kValues = MODE != kWeights;
+  constexpr int kYStride = (kValues ? 2 : 1) * S::kPageBytes;  // from a page of a slot to the next
+  constexpr int kSlot = kPair * kYStride;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_align<128>(smem_raw);
-  float *scores = reinterpret_cast<float *>(smem + S::kRing);  // [rows of this CTA][G] (ACC)
+  float *scores = reinterpret_cast<float *>(smem + W * kStages * kSlot);  // [pages of this CTA][G][16] (kStepWeights)
   __shared__ float m_s[kWarps * 8], l_s[kWarps * 8];
-  __shared__ AttnMerge mg;
+  __shared__ AttnMerge<W> mg;
   __shared__ __align__(8) uint64_t full[kWarps][kStages];
   __shared__ int abort_flag_s;
   volatile int *abort_flag = &abort_flag_s;
@@ -183,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
   const int n_pages = u.pg1 - u.pg0, first = u.pg0 + kPair * warp;
   const int n_my = n_pages > kPair * warp ? (n_pages - kPair * warp + kPair * kWarps - 1) / (kPair * kWarps) : 0;
   const int rows_end = min(u.len, u.pg1 * kPage);
-  uint8_t *ring = smem + warp * kStages * S::kSlot;
+  uint8_t *ring = smem + warp * kStages * kSlot;
 
   if (tid == 0) {
     for (int w = 0; w < kWarps; ++w)
@@ -202,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
   int ids = load_ids(0), ids_next = load_ids(32 / kPair);
   int ids_base = 0;
   const uint32_t ring_u = smem_u32(ring);
-  const int page_stride = p.hkv * S::kPageBytes;  // bytes from a page to the next in a pool
-  const uint8_t *pool = ((lane & 1) ? p.v_pool : p.k_pool) +
+  const int page_stride = p.hkv * S::kPageBytes;  // bytes from a page id to the next in a pool
+  const uint8_t *pool = (kValues && (lane & 1) ? p.v_pool : p.k_pool) +
                         ((int64_t)u.l * p.num_pages * p.hkv + u.h) * S::kPageBytes;  // page 0 of this unit
   auto issue_pair = [&](int k) {
     if (k >= ids_base + 32 / kPair) {
@@ -212,13 +200,14 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
       ids_next = load_ids(ids_base + 32 / kPair);
     }
     const int slot = k % kStages;
-    // lanes 0..3 copy K, V of the first page, K, V of the second
-    const int id = __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + (lane >> 1) % kPair);
-    const bool both = kPair == 1 || __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + kPair - 1) >= 0;
-    if (lane == 0) mbar_expect_tx(&full[warp][slot], (uint32_t)(both ? S::kSlot : S::kSlot / 2));
+    // lanes 0..3 copy K, V of the first page, K, V of the second; without values lanes 0 and 1 the pages' K
+    constexpr int kParts = kValues ? 2 : 1;
+    const int id = __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + (lane / kParts) % kPair);
+    const bool both = __shfl_sync(0xffffffffu, ids, kPair * (k - ids_base) + kPair - 1) >= 0;
+    if (lane == 0) mbar_expect_tx(&full[warp][slot], (uint32_t)(both ? kSlot : kSlot / 2));
     __syncwarp();
-    if (lane < (both ? 2 * kPair : 2))
-      bulk_load(ring_u + slot * S::kSlot + lane * S::kPageBytes, pool + (int64_t)id * page_stride,
+    if (lane < (both ? kParts * kPair : kParts))
+      bulk_load(ring_u + slot * kSlot + lane * S::kPageBytes, pool + (int64_t)id * page_stride,
                 (uint32_t)S::kPageBytes, &full[warp][slot]);
   };
   for (int k = 0; k < min(n_my, kStages); ++k) issue_pair(k);
@@ -240,11 +229,30 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) +
                         ((((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G + g) * D + t * (D / 16));
     float x[kInt4Groups][D / 16], top = 0.f, bad = 0.f, sum[kInt4Groups];
+    if (reinterpret_cast<uintptr_t>(p.q) % 16 == 0) {  // the unit in one read
+#pragma unroll
+      for (int gr = 0; gr < kInt4Groups; ++gr) {
+        uint32_t v[D / 32];
+        if constexpr (D == 128) {
+          const uint4 r = *reinterpret_cast<const uint4 *>(q + gr * (D / 4));
+          v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+        } else {
+          const uint2 r = *reinterpret_cast<const uint2 *>(q + gr * (D / 4));
+          v[0] = r.x, v[1] = r.y;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x[gr][2 * i] = bf16_lo(v[i]), x[gr][2 * i + 1] = bf16_hi(v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int gr = 0; gr < kInt4Groups; ++gr)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) x[gr][i] = bf16_lo(q[gr * (D / 4) + i]);
+    }
 #pragma unroll
     for (int gr = 0; gr < kInt4Groups; ++gr)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        x[gr][i] = bf16_lo(q[gr * (D / 4) + i]);
         top = fmaxf(top, fabsf(x[gr][i]));
         bad = fmaf(x[gr][i], 0.f, bad);  // NaN once a query value is infinite or NaN
       }
@@ -309,6 +317,12 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
   // rows of a page: fragment rows n and n + 8 are page rows ra and ra + 1, an
   // order in which no two lanes of a shared-memory phase meet in a bank
   const int ra = (n & 1) ? ((n + 3) & 7) + 8 : n;
+  [[maybe_unused]] float w_lse0 = 0.f, w_lse1 = 0.f;  // of columns 2t and 2t + 1
+  if constexpr (MODE == kWeights) {
+    const float *src = p.lse2 + ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
+    w_lse0 = 2 * t < G ? src[2 * t] : 0.f;
+    w_lse1 = 2 * t + 1 < G ? src[2 * t + 1] : 0.f;
+  }
   const int v0 = 2 * t, v1 = ((2 * t + 4) & 7) + 8;  // P's rows 2t and 2t + 1; v0 + 1 and v1 + 1 are 2t + 8 and 2t + 9
 
   float m0 = -INFINITY, m1 = -INFINITY;  // running maxima of columns 2t and 2t + 1 (base 2)
@@ -323,18 +337,31 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
   int k = 0;
   for (; k < n_my; ++k) {
     const int slot = k % kStages;
+    [[maybe_unused]] float2 w_old[kPair];
+    [[maybe_unused]] float *w_at[kPair];
+    if constexpr (MODE == kWeights) {  // lanes t = 0: the weights of rows ra and ra + 1, read ahead of the wait
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        const int pg = first + k * kPair * kWarps + y;
+        w_at[y] = nullptr;
+        if (t == 0 && pg < u.pg1 && pg * kPage + ra < u.len) {
+          w_at[y] = p.weights + (((int64_t)u.l * p.num_pages + u.bt[pg]) * p.hkv + u.h) * kPage + ra;
+          w_old[y] = *reinterpret_cast<const float2 *>(w_at[y]);
+        }
+      }
+    }
     const uint32_t parity = (uint32_t)((k / kStages) & 1);
     if (__any_sync(0xffffffffu, !mbar_try(&full[warp][slot], parity)) &&
         __any_sync(0xffffffffu, !mbar_wait(&full[warp][slot], parity, abort_flag, p.status)))
       break;
-    const uint8_t *base = ring + slot * S::kSlot;
+    const uint8_t *base = ring + slot * kSlot;
     const int valid = rows_end - (first + k * kPair * kWarps) * kPage;  // rows here; what lies past them is anything
 
     // 1. base-2 scores: s[y][0..1] of page row ra, [2..3] of row ra + 1, for columns 2t, 2t + 1
     float s[kPair][4];
 #pragma unroll
     for (int y = 0; y < kPair; ++y) {
-      const uint8_t *row0 = base + y * 2 * S::kPageBytes + ra * S::kRow, *row1 = row0 + S::kRow;
+      const uint8_t *row0 = base + y * kYStride + ra * S::kRow, *row1 = row0 + S::kRow;
       const uint4 h0 = *reinterpret_cast<const uint4 *>(row0), h1 = *reinterpret_cast<const uint4 *>(row1);
       const uint32_t ga[4] = {h0.x, h0.y, h0.z, h0.w}, gb[4] = {h1.x, h1.y, h1.z, h1.w};
       uint32_t wa[S::kWords], wb[S::kWords];
@@ -399,20 +426,38 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
         if (y * kPage + ra + 1 >= valid) s[y][2] = s[y][3] = -INFINITY;
       }
     }
-    if constexpr (ACC) {
+    if constexpr (MODE == kWeights) {
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        // lanes t and t ^ 2 hold the same heads where GP = 4; a repeated head counts once
+        const bool c0 = 2 * t < G, c1 = 2 * t + 1 < G;
+        float a = (c0 ? attn_ex2(s[y][0] - w_lse0) : 0.f) + (c1 ? attn_ex2(s[y][1] - w_lse1) : 0.f);
+        float b = (c0 ? attn_ex2(s[y][2] - w_lse0) : 0.f) + (c1 ? attn_ex2(s[y][3] - w_lse1) : 0.f);
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        b += __shfl_xor_sync(0xffffffffu, b, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
+        b += __shfl_xor_sync(0xffffffffu, b, 2);
+        if (w_at[y]) {
+          a = fmaf(p.decay, w_old[y].x, a);
+          b = fmaf(p.decay, w_old[y].y, b);
+          if (y * kPage + ra + 1 < valid)
+            *reinterpret_cast<float2 *>(w_at[y]) = make_float2(a, b);
+          else  // the last row: what lies past it stays
+            *w_at[y] = a;
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      if (k + kStages < n_my) issue_pair(k + kStages);
+      continue;
+    }
+    if constexpr (MODE == kStepWeights) {
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
         // the buffer holds whole pages: the second page of the last pair may lie past it
         if (y * kPage >= valid) continue;
-        float *dst = scores + ((kPair * (warp + k * kWarps) + y) * kPage + ra) * G + 2 * t;
-        if (2 * t < G) {
-          dst[0] = s[y][0];
-          dst[G] = s[y][2];
-        }
-        if (2 * t + 1 < G) {
-          dst[1] = s[y][1];
-          dst[G + 1] = s[y][3];
-        }
+        float *dst = scores + ((kPair * (warp + k * kWarps) + y) * G + 2 * t) * kPage + ra;
+        if (2 * t < G) *reinterpret_cast<float2 *>(dst) = make_float2(s[y][0], s[y][2]);
+        if (2 * t + 1 < G) *reinterpret_cast<float2 *>(dst + kPage) = make_float2(s[y][1], s[y][3]);
       }
     }
 
@@ -430,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
         n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
       }
-      const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);  // n0, n1 > -inf: a slot has a row
+      const float a0 = attn_ex2(m0 - n0), a1 = attn_ex2(m1 - n1);  // n0, n1 > -inf: a slot has a row
       m0 = n0;
       m1 = n1;
 #pragma unroll
@@ -451,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
     for (int y = 0; y < kPair; ++y)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float p0 = ex2(s[y][2 * x] - m0), p1 = ex2(s[y][2 * x + 1] - m1);
+        const float p0 = attn_ex2(s[y][2 * x] - m0), p1 = attn_ex2(s[y][2 * x + 1] - m1);
         const uint32_t h = pack_bf16(p0, p1);
         const float r0 = p0 - bf16_lo(h), r1 = p1 - bf16_hi(h);
         const uint32_t l = pack_bf16(r0, r1);
@@ -554,6 +599,11 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
         mbar_wait(&full[warp][j % kStages], (uint32_t)((j / kStages) & 1), abort_flag, p.status, false);
   }
 
+  if constexpr (MODE == kWeights) {
+    __syncthreads();  // a warp whose wait ran out has set the flag for the others by now
+    return;
+  }
+
   // the low terms of P sit two lanes on (GP = 4)
 #pragma unroll
   for (int i = 0; i < S::kTiles; ++i)
@@ -581,39 +631,79 @@ __global__ void __launch_bounds__(kThreads, KVC_ATTN4_MINB) decode_attention4_ke
     }
   }
   __syncthreads();
-  attn_finish<D, kWarps, kThreads>(p, u, G, red, m_s, l_s, mg, ACC ? scores : nullptr);
+  attn_finish<D, kWarps, kThreads>(p, u, G, red, m_s, l_s, mg, MODE == kStepWeights ? scores : nullptr);
 }
 
-template <int D, int GP, bool ACC>
-cudaError_t launch4(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
-  auto kernel = decode_attention4_kernel<D, GP, ACC>;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + Shape4<D>::kRing,
-                             ACC ? (size_t)kPage * G * 4 : 0, kThreads, s);
+// Cluster size: CTAs that share a unit, a power of two up to 16.  It grows
+//   * until a CTA's scores leave room for a second CTA on the SM (page_smem
+//     bytes a page, 0 without weights);
+//   * while the units are fewer than 1.5 CTAs per SM and every warp would keep
+//     two pages, or fewer than 4 and a CTA's share more than 64 pages;
+//   * until a CTA's share is at most 256 pages, so that requests of different
+//     lengths end together.
+// Measured for 4 warps a CTA (us; us at half and at twice the size): bf16 with
+// weights, 2048 units of 2048 rows: 1 CTA 347 (-, 408); 32 units of up to 8191
+// rows: 8 CTAs 29 (44, 34).  4 bits, 512 units of 4096 to 32768 rows, 8 heads:
+// 8 CTAs 563 (595, -); with weights and 4 heads 622 (891, 675); 64 units of 8192
+// rows: 8 CTAs 33 (36, -).
+int cluster_size(int64_t units, int np_max, int sms, int warps, size_t base_smem, size_t page_smem) {
+  int cs = 1;
+  while (cs < 16) {
+    const int share = (np_max + cs - 1) / cs;
+    const int64_t ctas = units * cs;
+    if (!(base_smem + page_smem * share > kSmemHalf || (2 * ctas < 3LL * sms && share > 2 * warps) ||
+          (ctas < 4LL * sms && share > 64) || share > 256))
+      break;
+    cs *= 2;
+  }
+  return cs;
+}
+
+template <int D, int GP, Mode4 MODE, int W>
+cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
+  auto kernel = decode_attention4_kernel<D, GP, MODE, W>;
+  const size_t slot = (size_t)kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + W * kStages * slot,
+                             MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W, MODE != kWeights, s);
+}
+
+// Without weights and with units enough to give every warp slot of the GPU one
+// and a half, a unit is one warp's: no merge, and the start and end of a unit
+// cost a quarter of what four warps pay (2048 rows, 4096 units: 296 us against
+// 322; 1024 units: 105 against 91).
+// With weights the scores stay in shared memory unless a CTA of the largest
+// cluster would have to keep more than 36 KB of them (more than 18432 rows at 8
+// heads): then too few warps fit an SM, and the weights take a launch of their
+// own that reads the keys again (64 requests of 4096 to 32768 rows, 8 heads:
+// KVC_TWO against 1211 us; at 4 heads, 622 us, one launch is the faster).
+template <int D, int GP>
+cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
+  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
+  if (!p.weights) {
+    if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1>(p, G, np_max, sms, s);
+    return launch4_w<D, GP, kStep, 4>(p, G, np_max, sms, s);
+  }
+  if (!p.lse2 || (size_t)kPage * G * 4 * ((np_max + 15) / 16) <= 36 * 1024)
+    return launch4_w<D, GP, kStepWeights, 4>(p, G, np_max, sms, s);
+  DecodeAttnParams step = p;
+  step.weights = nullptr;
+  if (cudaError_t e = launch4_w<D, GP, kStep, 4>(step, G, np_max, sms, s)) return e;
+  return launch4_w<D, GP, kWeights, 4>(p, G, np_max, sms, s);
 }
 
 }  // namespace
 
-// Picks the cluster size and launches a cluster-form attention kernel with
-// arguments (DecodeAttnParams, int G).
-//   base_smem: shared memory without the scores; page_smem: bytes of scores
-//   per page (0 without weights); np_max: most pages of a request.
-// The cluster is the smallest power of two up to 16 whose CTAs can hold their
-// rows' scores in shared memory and of which at least two waves fill the GPU,
-// as long as every warp keeps two pages: many units need no split, a few long
-// requests take all the SMs.
 cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
-                                size_t page_smem, int threads, cudaStream_t s) {
+                                size_t page_smem, int threads, bool cluster, cudaStream_t s) {
   constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // less the static shared memory
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (units <= 0) return cudaSuccess;
-  auto smem_of = [&](int cs) { return base_smem + page_smem * ((size_t)(np_max + cs - 1) / cs); };
-  int cs = 1;
-  while (cs < 16 && (smem_of(cs) > kMaxSmem || (units * cs < 4LL * sms && np_max > cs * 2 * (threads / 32)))) cs *= 2;
-  const size_t smem = smem_of(cs);
+  const int cs = cluster_size(units, np_max, sms, threads / 32, base_smem, page_smem);
+  const size_t smem = base_smem + page_smem * ((np_max + cs - 1) / cs);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-  if (cs > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+  if (cs > 8 && cluster && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
     return e;
   p.nsplit = cs;
   cudaLaunchConfig_t cfg{};
@@ -626,20 +716,15 @@ cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, 
   attr.val.clusterDim.x = (unsigned)cs;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
+  cfg.numAttrs = cs > 1 && cluster ? 1 : 0;
   void *args[] = {&p, &G};
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
 cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
                                      cudaStream_t s) {
-  const bool acc = p.weights != nullptr;
-  if (head_dim == 128) {
-    if (G <= 4) return acc ? launch4<128, 4, true>(p, G, np_max, sms, s) : launch4<128, 4, false>(p, G, np_max, sms, s);
-    return acc ? launch4<128, 8, true>(p, G, np_max, sms, s) : launch4<128, 8, false>(p, G, np_max, sms, s);
-  }
-  if (G <= 4) return acc ? launch4<64, 4, true>(p, G, np_max, sms, s) : launch4<64, 4, false>(p, G, np_max, sms, s);
-  return acc ? launch4<64, 8, true>(p, G, np_max, sms, s) : launch4<64, 8, false>(p, G, np_max, sms, s);
+  if (head_dim == 128) return G <= 4 ? launch4<128, 4>(p, G, np_max, sms, s) : launch4<128, 8>(p, G, np_max, sms, s);
+  return G <= 4 ? launch4<64, 4>(p, G, np_max, sms, s) : launch4<64, 8>(p, G, np_max, sms, s);
 }
 
 }  // namespace kvc
