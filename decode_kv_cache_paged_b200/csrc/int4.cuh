@@ -48,32 +48,46 @@ constexpr int kInt4Groups = 4;
 constexpr int kInt4Header = 16;  // bytes of the groups' words before the codes
 __host__ __device__ constexpr int int4_row_bytes(int d) { return d / 2 + kInt4Header; }
 
+// a / b from b's correctly rounded reciprocal: a product and one correction by
+// the remainder give the correctly rounded quotient (Markstein, IBM J. Res. Dev.
+// 34(1), 1990), barring overflow and underflow.  Both are harmless here: a
+// quotient that overflows is refused or NaN, one that underflows rounds to
+// code 0 like the exact one.
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+  const float q = a * inv;
+  return fmaf(fmaf(-q, b, a), inv, q);
+}
+
 // step of a group from its smallest and largest value
 __device__ __forceinline__ float int4_step(float lo, float hi) {
-  const float r = __fdiv_rn(hi - lo, 15.f);
+  const float r = quotient(hi - lo, 15.f, 1.f / 15.f);
   if (!(r < 0x1p56f)) return __int_as_float(0x7fffffff);  // NaN: infinities, NaN, a range too wide
   if (r < 0x1p-56f) return 0.f;
   return __uint_as_float((__float_as_uint(r) + 0xFFFFFu) & ~0xFFFFFu);
 }
 
-// a group's word from its step and lowest value (the step NaN for a broken group)
+// a group's word from its step, the step's reciprocal and its lowest value (the
+// step NaN for a broken group)
 template <bool IS_V>
-__device__ __forceinline__ uint32_t int4_word(float s, float lo) {
+__device__ __forceinline__ uint32_t int4_word(float s, float inv, float lo) {
   if (isnan(s)) return 0x7fffu;
   float z = 0.f;
   if (IS_V && s > 0.f) {
     const uint32_t e = __float_as_uint(s) & 0x7f800000u;      // 2^e
     const float x = -lo * __uint_as_float(0x7f000000u - e);  // -lo / 2^e
-    if (x > 0.f && x < 32.f) z = fminf(rintf(__fdiv_rn(-lo, s)), 15.f);
+    if (x > 0.f && x < 32.f) z = fminf(rintf(quotient(-lo, s, inv)), 15.f);
   }
   const float mid = fmaf(z, s, lo);
   return (__float_as_uint(s) & 0xfff00000u) | (uint32_t)z << 16 | __float_as_uint(mid) >> 16;
 }
 
+// a small integer as a float: 2^23 + n has n in its lowest bits
+__device__ __forceinline__ float small_float(uint32_t n) { return __uint_as_float(0x4b000000u | n) - 0x1p23f; }
+
 // what a group's word says: s, z * s (exact) and mid
 __device__ __forceinline__ void int4_unword(uint32_t h, float &s, float &zs, float &mid) {
   s = __uint_as_float(h & 0xfff00000u);
-  zs = (float)(h >> 16 & 15u) * s;
+  zs = small_float(h >> 16 & 15u) * s;
   mid = __uint_as_float(h << 16);
 }
 
