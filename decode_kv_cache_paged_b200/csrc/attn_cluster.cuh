@@ -126,7 +126,8 @@ __device__ __forceinline__ void attn_write_lse(const DecodeAttnParams &p, int64_
   if (p.lse2) p.lse2[head] = lse2;
 }
 
-// Merges the warps' and then the CTAs' states and writes the outputs.
+// Merges the warps' and then the CTAs' states and writes the outputs; with
+// p.part_o, the CTA's share for a merge launch instead (no cluster).
 //   red:  [W][G][D] the warps' sums, m_s, l_s: [W][G] their maxima and sums
 //         (a warp without rows has l = 0); the caller has synchronised.
 //   scores: [pages of this CTA][G][16] base-2 scores, or null (no weights).
@@ -136,7 +137,8 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
                                             const float *m_s, const float *l_s, AttnMerge<W> &mg, const float *scores) {
   const int tid = threadIdx.x;
   const int64_t head0 = ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
-  // the warps' factors; alone in its cluster a CTA divides by the sum at once
+  const bool alone = u.cs == 1 && !p.part_o;
+  // the warps' factors; a CTA that has the unit to itself divides by the sum at once
   for (int i = tid; i < W * 8; i += NT) {
     const int w = i >> 3, g = i & 7;
     if (g >= G) continue;
@@ -147,11 +149,16 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
     for (int x = 0; x < W; ++x)
       if (l_s[x * G + g] != 0.f) L = fmaf(l_s[x * G + g], attn_ex2(m_s[x * G + g] - M), L);
     const float f = l_s[w * G + g] != 0.f ? attn_ex2(m_s[w * G + g] - M) : 0.f;
-    mg.part[w][g] = u.cs > 1 || f == 0.f ? f : f / L;
+    mg.part[w][g] = !alone || f == 0.f ? f : f / L;
     if (w == 0) {
       mg.m[g] = M;
       mg.l[g] = L;
-      if (u.cs == 1) {
+      if (p.part_o) {
+        const int64_t pu = (head0 + g) * u.cs + u.rank;
+        p.part_ml[pu * 2] = M;
+        p.part_ml[pu * 2 + 1] = L;
+      }
+      if (alone) {
         const float lse2 = M + log2f(L);
         mg.lse2[g] = lse2;
         attn_write_lse(p, head0 + g, u.len > 0 ? lse2 : -INFINITY);
@@ -166,11 +173,14 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
       const float f = mg.part[w][i / D];
       if (f != 0.f) o = fmaf(red[w * G * D + i], f, o);
     }
-    if (u.cs > 1)
+    if (p.part_o)
+      p.part_o[((head0 + i / D) * u.cs + u.rank) * D + i % D] = o;
+    else if (u.cs > 1)
       red[i] = o;
     else
       p.out[head0 * D + i] = o;
   }
+  if (p.part_o) return;
   if (u.cs > 1) {
     cluster_sync_all();
     for (int i = tid; i < u.cs * 8; i += NT) {

@@ -51,6 +51,7 @@ namespace {
 #endif
 
 constexpr int kThreads = 128;
+constexpr int kMaxSplits = 16;  // splits of a unit, at most
 constexpr float kLn2 = 0.6931471805599453f;
 
 // bf16 pair / fp32 pair of a 32-bit or 64-bit word as a float2
@@ -478,27 +479,34 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   }
 }
 
-// merge the splits of one (layer, request, KV head): G*D outputs
-__global__ void __launch_bounds__(kThreads) decode_attention_merge_kernel(DecodeAttnParams p, int G, int D) {
-  const int64_t head0 = (int64_t)blockIdx.x * G;
-  for (int i = threadIdx.x; i < G * D; i += kThreads) {
-    const int g = i / D, c = i % D;
-    const int64_t pu0 = (head0 + g) * p.nsplit;
-    float m = -INFINITY;
-    for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, p.part_ml[(pu0 + s) * 2]);
-    float o = 0.f, l = 0.f;
-    if (m != -INFINITY) {
-      for (int s = 0; s < p.nsplit; ++s) {
-        const float ms = p.part_ml[(pu0 + s) * 2];
-        if (ms == -INFINITY) continue;
-        const float w = exp2f(ms - m);
-        l = fmaf(p.part_ml[(pu0 + s) * 2 + 1], w, l);
-        o = fmaf(p.part_o[(pu0 + s) * D + c], w, o);
-      }
-    }
-    p.out[(head0 + g) * D + c] = l > 0.f ? o / l : 0.f;
-    if (p.lse && c == 0) p.lse[head0 + g] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+// Merges the splits of one (layer, request, query head): a thread per output
+// dimension.  Every partial is read before the first is used, so the launch
+// waits for memory twice and not once per split (one bf16 request of 32768 rows,
+// 8 KV heads, 16 splits: 48 us for the step, 69 with a loop per output).
+__global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D) {
+  const int64_t head = blockIdx.x, pu0 = head * p.nsplit;
+  const int c = threadIdx.x;
+  float ms[kMaxSplits], ls[kMaxSplits], os[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const bool on = s < p.nsplit;
+    ms[s] = on ? p.part_ml[(pu0 + s) * 2] : -INFINITY;
+    ls[s] = on ? p.part_ml[(pu0 + s) * 2 + 1] : 0.f;
+    os[s] = on ? p.part_o[(pu0 + s) * D + c] : 0.f;
   }
+  float m = -INFINITY, o = 0.f, l = 0.f;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) m = fmaxf(m, ms[s]);
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    if (ls[s] == 0.f) continue;  // no rows
+    const float w = exp2f(ms[s] - m);
+    l = fmaf(ls[s], w, l);
+    o = fmaf(os[s], w, o);
+  }
+  const bool none = l == 0.f;
+  p.out[head * D + c] = none ? 0.f : o / l;
+  if (p.lse && c == 0) p.lse[head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int G>
@@ -514,6 +522,7 @@ cudaError_t launch_typed(const DecodeAttnParams &p, int units, cudaStream_t s) {
 template <typename T, int D, int G>
 cudaError_t launch_acc(DecodeAttnParams p, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention_kernel<T, D, G, true>;
+  p.part_o = p.part_ml = nullptr;
   return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, AttnShape<T, D, G>::kSmem,
                              (size_t)kPage * G * 4, kThreads, true, s);
 }
@@ -553,6 +562,11 @@ cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim,
   return head_dim == 128 ? launch_acc_g<float, 128>(p, G, np_max, sms, s) : launch_acc_g<float, 64>(p, G, np_max, sms, s);
 }
 
+cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, cudaStream_t s) {
+  decode_attention_merge_kernel<<<p.layer_count * p.R * p.hq, head_dim, 0, s>>>(p, head_dim);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s) {
   *launches = 0;
@@ -566,9 +580,7 @@ cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int
   if (e != cudaSuccess) return e;
   *launches = 1;
   if (p.nsplit > 1) {
-    decode_attention_merge_kernel<<<p.layer_count * p.R * p.hkv, kThreads, 0, s>>>(p, G, head_dim);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if ((e = launch_decode_attention_merge(p, head_dim, s)) != cudaSuccess) return e;
     *launches = 2;
   }
   return cudaSuccess;

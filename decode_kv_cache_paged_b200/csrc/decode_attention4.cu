@@ -52,13 +52,14 @@
 // Every mbarrier wait is bounded (tc_ptx.cuh).
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "attn_cluster.cuh"
 #include "int4.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kStages = 2;  // slots per warp
 constexpr size_t kSmemHalf = 111 * 1024;  // dynamic shared memory with which two CTAs fit an SM
 constexpr int kPair = 2;    // pages per slot
 
@@ -148,10 +149,10 @@ enum Mode4 { kStep, kStepWeights, kWeights };
 
 // GP: columns of the product that hold query heads, 4 (G <= 4: the second parts
 // take the other four) or 8.  W: warps of a CTA; 16 warps fit an SM.
-template <int D, int GP, Mode4 MODE, int W>
+template <int D, int GP, Mode4 MODE, int W, int ST>
 __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16) / W) decode_attention4_kernel(DecodeAttnParams p, int G) {
   using S = Shape4<D>;
-  constexpr int kWarps = W, kThreads = 32 * W;
+  constexpr int kWarps = W, kThreads = 32 * W, kStages = ST;
   constexpr bool kValues = MODE != kWeights;
   constexpr int kYStride = (kValues ? 2 : 1) * S::kPageBytes;  // from a page of a slot to the next
   constexpr int kSlot = kPair * kYStride;
@@ -659,36 +660,59 @@ int cluster_size(int64_t units, int np_max, int sms, int warps, size_t base_smem
   return cs;
 }
 
-template <int D, int GP, Mode4 MODE, int W>
+template <int D, int GP, Mode4 MODE, int W, int ST>
 cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
-  auto kernel = decode_attention4_kernel<D, GP, MODE, W>;
+  auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
+  p.part_o = p.part_ml = nullptr;
   const size_t slot = (size_t)kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + W * kStages * slot,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + W * ST * slot,
                              MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W, MODE != kWeights, s);
+}
+
+// A unit split over `splits` CTAs of 8 warps that are no cluster, and a launch
+// that merges them.
+template <int D, int GP>
+cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s) {
+  auto kernel = decode_attention4_kernel<D, GP, kStep, 8, 2>;
+  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
+  const size_t smem = 128 + 8 * 2 * (size_t)Shape4<D>::kSlot;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  p.nsplit = splits;
+  p.part_ml = p.part_o + (size_t)p.layer_count * p.R * p.hq * splits * D;
+  kernel<<<(unsigned)(units * splits), 256, smem, s>>>(p, G);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_decode_attention_merge(p, D, s);
 }
 
 // Without weights and with units enough to give every warp slot of the GPU one
 // and a half, a unit is one warp's: no merge, and the start and end of a unit
 // cost a quarter of what four warps pay (2048 rows, 4096 units: 296 us against
 // 322; 1024 units: 105 against 91).
+// A few long requests are split without a cluster: the SMs take at most seven
+// clusters of 16 with a CTA each, so that clusters share SMs while others idle
+// (8 units of 32768 rows: 26 us against 36).
 // With weights the scores stay in shared memory unless a CTA of the largest
 // cluster would have to keep more than 36 KB of them (more than 18432 rows at 8
 // heads): then too few warps fit an SM, and the weights take a launch of their
 // own that reads the keys again (64 requests of 4096 to 32768 rows, 8 heads:
-// KVC_TWO against 1211 us; at 4 heads, 622 us, one launch is the faster).
+// 800 us against 1019; 4 heads, 32 KB each: 39 us against 54 for one request in
+// one launch, 625 against 619 for the 64).
 template <int D, int GP>
 cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (!p.weights) {
-    if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1>(p, G, np_max, sms, s);
-    return launch4_w<D, GP, kStep, 4>(p, G, np_max, sms, s);
+    if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1, 2>(p, G, np_max, sms, s);
+    const int splits = std::min({p.max_splits, (np_max + 15) / 16, (int)(2LL * sms / units)});
+    if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP>(p, G, splits, s);
+    return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
   }
   if (!p.lse2 || (size_t)kPage * G * 4 * ((np_max + 15) / 16) <= 36 * 1024)
-    return launch4_w<D, GP, kStepWeights, 4>(p, G, np_max, sms, s);
+    return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
-  if (cudaError_t e = launch4_w<D, GP, kStep, 4>(step, G, np_max, sms, s)) return e;
-  return launch4_w<D, GP, kWeights, 4>(p, G, np_max, sms, s);
+  if (cudaError_t e = launch4_w<D, GP, kStep, 4, 2>(step, G, np_max, sms, s)) return e;
+  return launch4_w<D, GP, kWeights, 4, 2>(p, G, np_max, sms, s);
 }
 
 }  // namespace

@@ -944,6 +944,7 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   p.qscale = (scale > 0.f ? scale : 1.0f / std::sqrt((float)c.head_dim)) * 1.4426950408889634f;
   p.weights = o.accumulate ? ctx->weights : nullptr;
   p.decay = o.decay;
+  p.max_splits = kAttnSplits / layer_count;
   // scratch of the partials region; a layer's share of it holds d + 2 times 16 floats per query head
   p.lse2 = o.accumulate && layer_count <= (c.head_dim + 2) * kAttnSplits ? ctx->d_attn : nullptr;
   if (ms_out) KVC_CUDA(ctx, cudaEventRecord(ctx->ev[0], ctx->stream));

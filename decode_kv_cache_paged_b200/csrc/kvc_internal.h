@@ -70,6 +70,7 @@ struct DecodeAttnParams {
   float qscale;                // scale * log2(e)
   float *weights;              // accumulated attention weights, indexed like the position map, or null
   float decay;                 // weights <- decay * weights + this step's
+  int32_t max_splits;          // splits of a unit that part_o and part_ml have room for
   float *lse2;                 // scratch [layer_count][R][Hq]: log2-sum-exp2 for a weights launch of its own, or null
 };
 
@@ -131,6 +132,7 @@ cudaError_t launch_gather_dense(const uint8_t *k_pool, const uint8_t *v_pool,
                                 int cap, int hkv, int row_bytes, int64_t num_pages, int bt_stride,
                                 uint8_t *k_out, uint8_t *v_out, int32_t *pos_out, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(int32_t *status, uint32_t limit_ms, cudaStream_t s);
+cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, cudaStream_t s);
 bool decode_attention_supported(int dtype, int head_dim, int G);
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s);

@@ -1,15 +1,13 @@
 """The 4-bit cache: its rows bit for bit, decode attention over them, rounds that move them.
 
-Tolerance of the attention (u = 2^-24).  The operands q and step*code have at most 8 significant bits each, so their
-products are exact in fp32; the tensor cores add 16 of them to an fp32 accumulator and may truncate, so each of the
-d/16 + 1 additions errs by at most 2u of the magnitudes it holds.  The group sums of q that multiply lo are fp32 sums of
-at most 32 terms, and scaling, the running maximum's subtraction and exp2 add three roundings.  With
-A = max_j scale*(sum_i |q_i| step code_ji + sum_g |lo_jg| sum_{i in g} |q_i|):
-  score error  ds <= (2*(d/16 + 1) + 8) * 2u * A + 2u*|s - m| + 4u.
-A weight enters the second product as the sum of two bf16 numbers, off by at most 2^-9 * 2^-9 = 2^-18 of itself (the
-normaliser adds the same rounded weights); its sums take L/16 additions of 2u each in one chain at most, the merges of
-the warps and CTAs 64 more roundings.  The product's terms are step*code and lo, at most 3 max|v| together:
-  out error    <= 3 max_j|v_jc| * (2 ds + 2 * 2^-18 + 2*(L/16 + 64)*2u),
+Tolerance of the attention (u = 2^-24).  The scores' products of codes and the integer parts of the query are exact, and
+so are their sums (integers below 2^21); the rest of the query is at most 1/2 beside integers up to 2047 and its 16-term
+products may lose 2u of their largest each.  s and lo join them in fp32: 12 roundings per score, scaling, the subtraction of
+the maximum and exp2 add four.  With A = max_j scale*(sum_i |q_i| step code_ji + sum_g |lo_jg| sum_{i in g} |q_i|):
+  score error  ds <= 16 u A + 2u*|s - m| + 4u; 4 (d/16 + 5) u A is used, which is above it.
+A weight enters the second product as three bf16 numbers that hold all of its bits; the tensor cores may truncate 2u of the
+largest of 16 products each, in a chain of at most 6, and the running sums take L/32 additions, the merges 64 more:
+  out error    <= 3 max_j|v_jc| * (2 ds + 2 * 2^-18 + 2*(L/16 + 64)*2u),  (2^-18 = 64u covers the products' truncation)
   lse error    <= ds + 2^-18 + (L/16 + 64)*2u + 4u|lse|."""
 import numpy as np
 import pytest
@@ -197,6 +195,68 @@ def test_attention_many_units():
     out, lse = ctx.decode_attention(q, layer_begin=1, scale=0.3)
     ctx.sync()
     print(check_attention(ctx, q, out, lse, [1, 2], 0.3))
+    ctx.close()
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_attention_one_warp_units(G):
+    """Units enough for the form with one warp a unit: lengths around the pairs of pages a warp takes."""
+    lens = [(7 * i) % 70 for i in range(60)]
+    ctx = make(lens, layers=8, H=8, G=G, d=64)
+    fill(ctx, lens, seed=45)
+    q = rows(len(lens), 8, 8 * G, 64, 8)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, range(8), 64 ** -0.5))
+    ctx.close()
+
+
+def test_unaligned_queries():
+    """Queries on a 2-byte boundary, as the call allows, give the same bits."""
+    ctx = make([70, 300], H=2, G=4)
+    fill(ctx, [70, 300], seed=46)
+    q = rows(2, 1, 8, 128, 9)[0].contiguous()
+    a = ctx.decode_attention(q)
+    odd = torch.empty(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
+    odd.copy_(q)
+    assert odd.data_ptr() % 16 == 2
+    b = ctx.decode_attention(odd)
+    ctx.sync()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ctx.close()
+
+
+def test_query_ranges():
+    """Query values 30 binades apart, tiny and huge queries, and a zero query in one batch."""
+    lens = [40, 90, 33, 50]
+    ctx = make(lens, H=2, G=4)
+    fill(ctx, lens, seed=47, kind="normal")
+    q = rows(4, 1, 8, 128, 10)[0].float()
+    q[:, 0] *= torch.where(torch.arange(128, device="cuda") % 3 == 0, 2.0 ** -30, 1.0)
+    q[:, 1] *= 2.0 ** -100
+    q[:, 2] *= 16.0
+    q[:, 3] = 0
+    q = q.bfloat16()
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
+    ctx.close()
+
+
+def test_broken_queries_stay_in_their_rows():
+    """An infinite or NaN query value makes its own head's row NaN and no other."""
+    ctx = make([50], H=2, G=4)
+    fill(ctx, [50], seed=48)
+    q = rows(1, 1, 8, 128, 11)[0]
+    want = ctx.decode_attention(q)
+    for bad in (float("inf"), float("nan")):
+        x = q.clone()
+        x[0, 0, 5, 77] = bad
+        out, lse = ctx.decode_attention(x)
+        ctx.sync()
+        keep = [i for i in range(8) if i != 5]
+        assert torch.isnan(out[0, 0, 5]).all() and torch.isnan(lse[0, 0, 5])
+        assert torch.equal(out[0, 0, keep], want[0][0, 0, keep]) and torch.equal(lse[0, 0, keep], want[1][0, 0, keep])
     ctx.close()
 
 
