@@ -60,7 +60,8 @@
 namespace kvc {
 namespace {
 
-constexpr size_t kSmemHalf = 111 * 1024;  // dynamic shared memory with which two CTAs fit an SM
+constexpr size_t kSmemHalf = 111 * 1024;        // dynamic shared memory with which two CTAs fit an SM
+constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // the most for one, less the static shared memory
 constexpr int kPair = 2;    // pages per slot
 
 template <int D>
@@ -637,7 +638,8 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
 
 // Cluster size: CTAs that share a unit, a power of two up to 16.  It grows
 //   * until a CTA's scores leave room for a second CTA on the SM (page_smem
-//     bytes a page, 0 without weights);
+//     bytes a page, 0 without weights), or only fit at all where the page slots
+//     alone take half of it (fp32 rows of 128 channels);
 //   * while the units are fewer than 1.5 CTAs per SM and every warp would keep
 //     two pages, or fewer than 4 and a CTA's share more than 64 pages;
 //   * until a CTA's share is at most 256 pages, so that requests of different
@@ -648,11 +650,12 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
 // 8 CTAs 563 (595, -); with weights and 4 heads 622 (891, 675); 64 units of 8192
 // rows: 8 CTAs 33 (36, -).
 int cluster_size(int64_t units, int np_max, int sms, int warps, size_t base_smem, size_t page_smem) {
+  const size_t room = base_smem + 16 * 1024 > kSmemHalf ? kMaxSmem : kSmemHalf;
   int cs = 1;
   while (cs < 16) {
     const int share = (np_max + cs - 1) / cs;
     const int64_t ctas = units * cs;
-    if (!(base_smem + page_smem * share > kSmemHalf || (2 * ctas < 3LL * sms && share > 2 * warps) ||
+    if (!(base_smem + page_smem * share > room || (2 * ctas < 3LL * sms && share > 2 * warps) ||
           (ctas < 4LL * sms && share > 64) || share > 256))
       break;
     cs *= 2;
@@ -719,7 +722,6 @@ cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaS
 
 cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
                                 size_t page_smem, int threads, bool cluster, cudaStream_t s) {
-  constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // less the static shared memory
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (units <= 0) return cudaSuccess;
   const int cs = cluster_size(units, np_max, sms, threads / 32, base_smem, page_smem);

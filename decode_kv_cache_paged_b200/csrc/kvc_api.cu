@@ -909,7 +909,10 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   const int R = c.num_requests;
   int max_len = 0;
   for (int r = 0; r < R; ++r) max_len = std::max(max_len, ctx->h_len[r]);
-  const int np_max = (max_len + kPage - 1) / kPage;
+  // a captured step may be replayed over a longer cache than today's
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
+  const int np_max = cap == cudaStreamCaptureStatusNone ? (max_len + kPage - 1) / kPage : ctx->maxp;
   // splits: enough CTAs for two waves of two CTAs per SM, pages of a split a
   // multiple of the 4-page tile, at least two tiles per split
   const int64_t base = (int64_t)layer_count * R * c.num_kv_heads;
@@ -953,12 +956,8 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   if (c.dtype != KVC_INT4 && !o.accumulate) {
     e = launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream);
   } else {
-    // a captured step may be replayed over a longer cache than today's
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
-    const int pages = cap == cudaStreamCaptureStatusNone ? np_max : ctx->maxp;
-    e = c.dtype == KVC_INT4 ? launch_decode_attention4(p, c.head_dim, G, pages, ctx->num_sms, ctx->stream)
-                            : launch_decode_attention_acc(p, c.head_dim, c.dtype, G, pages, ctx->num_sms, ctx->stream);
+    e = c.dtype == KVC_INT4 ? launch_decode_attention4(p, c.head_dim, G, np_max, ctx->num_sms, ctx->stream)
+                            : launch_decode_attention_acc(p, c.head_dim, c.dtype, G, np_max, ctx->num_sms, ctx->stream);
   }
   if (e != cudaSuccess) return cuda_fail(ctx, e, "decode_attention");
   if (ms_out) {

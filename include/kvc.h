@@ -324,7 +324,8 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *     out = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Slot order does not matter (rows after hole filling included).  A request
  * with no rows gets out = 0 and lse = -inf.
- * Over a KVC_INT4 cache k_j and v_j are the values that the codes stand for.
+ * Over a KVC_INT4 cache k_j and v_j are the values that the codes stand for,
+ * and query values are to stay below 2^100 in size.
  *   q:   device [layer_count][num_requests][num_q_heads][head_dim] in the
  *        cache dtype (bf16 for KVC_INT4), element-aligned; read only.
  *   scale: > 0, or 0 for 1/sqrt(head_dim).
@@ -334,7 +335,10 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *   ms_out: host float or NULL; if given, the call synchronises and writes
  *     the device time of its kernels, and reports latched device errors.
  * Enqueued on the context's stream; uses the context's workspace for split
- * partials, so calls on one context must not overlap.  Errors (nothing
+ * partials, so calls on one context must not overlap.  Without ms_out the call
+ * may be captured into a CUDA graph (after one call outside a capture, which
+ * loads the kernels); a replay reads the cache as it stands then, rows appended
+ * and rounds made since the capture included.  Errors (nothing
  * enqueued): KVC_ERR_INVALID_ARG; KVC_ERR_UNSUPPORTED unless head_dim is 64
  * or 128 and G in {1, 2, 4, 8}. */
 kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,

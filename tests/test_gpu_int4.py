@@ -375,12 +375,13 @@ def test_the_same_call_gives_the_same_bits():
     ctx.close()
 
 
-def test_captured_step_follows_the_cache():
+@pytest.mark.parametrize("dtype", ["int4", torch.bfloat16], ids=str)
+def test_captured_step_follows_the_cache(dtype):
     """A captured step replays over the cache as it then stands: more rows, other queries."""
     lens = [100, 900]
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
-        ctx = make(lens, H=2, G=4, room=2000)
+        ctx = make(lens, H=2, G=4, room=2000, dtype=dtype)
         fill(ctx, lens, seed=120)
         q = rows(2, 1, 8, 128, 15)[0]
         out, lse = ctx.decode_attention(q)  # the first call sets the kernels up
@@ -394,6 +395,53 @@ def test_captured_step_follows_the_cache():
         side.synchronize()
         print(check_attention(ctx, q, out, lse, [0], 128 ** -0.5))
         side.synchronize()
+    ctx.close()
+
+
+@pytest.mark.parametrize("room", [0, 30000])
+def test_two_captured_steps_share_the_context(room):
+    """Two captured steps of other layers and queries, replayed one after the other in both orders."""
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ctx = make([700, 300], layers=2, H=2, G=4, room=room)
+        fill(ctx, [700, 300], seed=125)
+        qs = [rows(2, 1, 8, 128, 20 + i)[0] for i in range(2)]
+        res = [ctx.decode_attention(qs[i], layer_begin=i) for i in range(2)]
+        side.synchronize()
+        graphs = []
+        for i in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                ctx.decode_attention(qs[i], layer_begin=i, out=res[i][0], lse=res[i][1])
+            graphs.append(g)
+        for order in ((0, 1), (1, 0)):
+            for o in res:
+                o[0].zero_()
+            for i in order:
+                graphs[i].replay()
+            side.synchronize()
+            for i in range(2):
+                check_attention(ctx, qs[i], res[i][0], res[i][1], [i], 128 ** -0.5)
+        side.synchronize()
+    ctx.close()
+
+
+def test_pools_past_4_gb():
+    """Row addresses past 2^32 bytes: the last layers of pools of 6 GB."""
+    ctx = make([100, 47], layers=4, H=8, G=4, extra_pages=150000)
+    assert ctx.k_pool.numel() > 6 * 10 ** 9
+    given = fill(ctx, [100, 47], seed=135)
+    w = ctx.track_weights()
+    q = rows(2, 1, 32, 128, 30)[0]
+    out, lse = ctx.decode_attention(q, layer_begin=3, accumulate=True)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, [3], 128 ** -0.5))
+    k, _, _ = ctx.gather_dense(3)
+    assert np.array_equal(k[0, :, :100].cpu().numpy(), rows4.row_values(np64(given[0][0][3]).transpose(1, 0, 2)).astype(np.float32))
+    assert abs(float(w[3].sum()) - 2 * 32) < 1e-2 and not w[:3].any()  # each query head's weights sum to 1
+    ctx.compress("attention", np.array([40, 40], np.int32), 0)
+    ctx.sync()
+    assert ctx.lengths()[0].tolist() == [40, 40]
     ctx.close()
 
 
