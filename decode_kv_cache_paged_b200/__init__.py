@@ -192,7 +192,11 @@ class Context:
     ``dtype`` is the cache's: torch.bfloat16, torch.float32, or "int4" for the
     4-bit cache (KVC_INT4), whose K, V and queries are bfloat16 and whose pools
     hold the coded rows as bytes.  ``self.dtype`` is the type of the K, V and
-    query tensors; ``self.weights`` the tracked attention weights or None."""
+    query tensors; ``self.weights`` the tracked attention weights or None.
+
+    Work is enqueued on ``stream`` (torch's current one unless given).  The tensors
+    that the methods take, copy and return belong to torch's current stream: where
+    that is another one, the caller orders the two."""
 
     def __init__(self, spec: ContextSpec, dtype=None, device="cuda", stream=None):
         import torch

@@ -10,7 +10,8 @@
 // sit in its shared memory: the weights exp2(score - lse) then cost one read
 // and one write of 4 bytes per row, and no second pass over the keys.  The
 // share comes from the request's length on the device, so a captured launch
-// follows the cache.
+// follows the cache.  With p.part_o the CTAs of a unit are no cluster and leave
+// their states for a merge launch (few long requests, decode_attention4.cu).
 #pragma once
 #include "kvc_internal.h"
 #include "tc_ptx.cuh"

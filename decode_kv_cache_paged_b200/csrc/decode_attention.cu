@@ -483,7 +483,9 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
 // dimension.  Every partial is read before the first is used, so the launch
 // waits for memory twice and not once per split (one bf16 request of 32768 rows,
 // 8 KV heads, 16 splits: 48 us for the step, 69 with a loop per output).
-__global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D) {
+// A sum that is NaN counts as no rows, as in a step without splits, unless
+// keep_nan (the 4-bit cache, whose broken groups show as NaN).
+__global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D, bool keep_nan) {
   const int64_t head = blockIdx.x, pu0 = head * p.nsplit;
   const int c = threadIdx.x;
   float ms[kMaxSplits], ls[kMaxSplits], os[kMaxSplits];
@@ -504,7 +506,7 @@ __global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D) {
     l = fmaf(ls[s], w, l);
     o = fmaf(os[s], w, o);
   }
-  const bool none = l == 0.f;
+  const bool none = !(l > 0.f) && !(keep_nan && isnan(l));
   p.out[head * D + c] = none ? 0.f : o / l;
   if (p.lse && c == 0) p.lse[head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -562,8 +564,8 @@ cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim,
   return head_dim == 128 ? launch_acc_g<float, 128>(p, G, np_max, sms, s) : launch_acc_g<float, 64>(p, G, np_max, sms, s);
 }
 
-cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, cudaStream_t s) {
-  decode_attention_merge_kernel<<<p.layer_count * p.R * p.hq, head_dim, 0, s>>>(p, head_dim);
+cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, bool keep_nan, cudaStream_t s) {
+  decode_attention_merge_kernel<<<p.layer_count * p.R * p.hq, head_dim, 0, s>>>(p, head_dim, keep_nan);
   return cudaGetLastError();
 }
 
@@ -580,7 +582,7 @@ cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int
   if (e != cudaSuccess) return e;
   *launches = 1;
   if (p.nsplit > 1) {
-    if ((e = launch_decode_attention_merge(p, head_dim, s)) != cudaSuccess) return e;
+    if ((e = launch_decode_attention_merge(p, head_dim, false, s)) != cudaSuccess) return e;
     *launches = 2;
   }
   return cudaSuccess;

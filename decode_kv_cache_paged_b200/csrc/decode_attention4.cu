@@ -685,7 +685,7 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
   p.part_ml = p.part_o + (size_t)p.layer_count * p.R * p.hq * splits * D;
   kernel<<<(unsigned)(units * splits), 256, smem, s>>>(p, G);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_decode_attention_merge(p, D, s);
+  return launch_decode_attention_merge(p, D, true, s);
 }
 
 // Without weights and with units enough to give every warp slot of the GPU one
@@ -728,7 +728,8 @@ cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, 
   const size_t smem = base_smem + page_smem * ((np_max + cs - 1) / cs);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  // the same limit for every launch: two threads' calls may interleave
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem)) != cudaSuccess) return e;
   if (cs > 8 && cluster && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
     return e;
   p.nsplit = cs;

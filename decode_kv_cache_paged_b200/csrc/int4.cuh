@@ -35,7 +35,7 @@
 // without, below 1e-6 with it).  mid is exact: where z > 0 it is a multiple of
 // lo's last place (which is at most s's) and no larger than max(|lo|, s / 2).
 // A K row's sums over channels are short, and its codes enter the products
-// without s, as 8-bit floats, so there z would only cost; their order puts
+// without s, as fp16 numbers, so there z would only cost; their order puts
 // what one lane of those products reads side by side.  The limits of s keep
 // s * 2^64 and s / 2^64 within bf16's normal numbers (decode_attention4.cu).
 #pragma once

@@ -870,6 +870,10 @@ kvc_status kvc_bind_weights(kvc_ctx *ctx, float *weights, size_t weights_bytes) 
   KVC_CUDA(ctx, cudaSetDevice(ctx->device));
   if (!device_ptr_on(ctx->device, weights))
     return fail(ctx, KVC_ERR_INVALID_ARG, "weights must be device memory of the context's device");
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(ctx, KVC_ERR_STATE, "weights cannot be bound while the stream is being captured");
   KVC_CUDA(ctx, cudaMemsetAsync(weights, 0, need, ctx->stream));
   ctx->weights = weights;
   return KVC_OK;

@@ -264,7 +264,7 @@ __device__ __forceinline__ uint32_t sc_weight_key(const SelectCompactParams &p, 
     atomicCAS(p.status, kDevOk, kDevNaN);
     return 0u;
   }
-  return float_order_key(w);
+  return float_order_key(w + 0.f);  // -0 is 0
 }
 
 // The 4-byte word that moves with each row beside its K and V: a row's first

@@ -325,7 +325,7 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  * Slot order does not matter (rows after hole filling included).  A request
  * with no rows gets out = 0 and lse = -inf.
  * Over a KVC_INT4 cache k_j and v_j are the values that the codes stand for,
- * and query values are to stay below 2^100 in size.
+ * and the queries and values are to stay below 2^100 in size.
  *   q:   device [layer_count][num_requests][num_q_heads][head_dim] in the
  *        cache dtype (bf16 for KVC_INT4), element-aligned; read only.
  *   scale: > 0, or 0 for 1/sqrt(head_dim).
@@ -354,7 +354,8 @@ kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer
  *     A step adds G per (request, layer, KV head) in all.  Rows past a
  *     request's length are left as they are.
  *   decay: in [0, 1]; 1 gives the plain sum over the steps, 0 the last step's
- *     weights.  Ignored without accumulate.
+ *     weights (where they were finite: decay * w_j is a product like any
+ *     other).  Ignored without accumulate.
  *   reserved: 0. */
 typedef struct kvc_attention_options {
   int32_t accumulate;
@@ -379,8 +380,9 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
  * new rows at 0, rounds move the weights with their rows, and
  * kvc_decode_attention_ex adds to them; the caller may read or write them in
  * stream order, for instance where another attention backend supplies them.
- * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_UNSUPPORTED unless head_dim is 64 or
- * 128. */
+ * A captured step keeps the buffer that was bound at its capture.
+ * Errors: KVC_ERR_INVALID_ARG; KVC_ERR_UNSUPPORTED unless head_dim is 64 or
+ * 128; KVC_ERR_STATE while the context's stream is being captured. */
 kvc_status kvc_bind_weights(kvc_ctx *ctx, float *weights, size_t weights_bytes);
 
 /* Fills *out with device pointers to the live state (no copy, no sync). */

@@ -339,6 +339,49 @@ def test_infinite_weights_and_zero_weights():
     ctx.close()
 
 
+def test_negative_zero_is_zero():
+    """Weights of -0 and 0 are equal scores: the lowest positions stay."""
+    for n in (80, 4200):  # the one-CTA form and the persistent one
+        ctx = make([n], H=2, d=64, dtype=torch.bfloat16)
+        fill(ctx, [n], seed=48)
+        w = ctx.track_weights()
+        w.view(-1)[::2] = -0.0
+        ctx.compress("attention", np.array([n // 3], np.int32), 0)
+        ctx.sync()
+        assert ctx.gather_dense(0, cap=n // 3)[2][0, 1].tolist() == list(range(n // 3))
+        ctx.close()
+
+
+def test_contexts_on_two_streams():
+    """Two contexts of other sizes, their calls interleaved on two streams, give the bits of each alone."""
+    sizes = [([6000, 10], 8, 128, "int4"), ([300, 257, 0], 2, 64, "int4"), ([5000], 4, 128, torch.bfloat16)]
+    alone = []
+    for together in (False, True):
+        streams = [torch.cuda.Stream() for _ in sizes] if together else [torch.cuda.current_stream()] * len(sizes)
+        ctxs, qs, got = [], [], []
+        for i, (lens, G, d, dtype) in enumerate(sizes):
+            with torch.cuda.stream(streams[i]):
+                ctxs.append(make(lens, H=2, G=G, d=d, dtype=dtype))
+                fill(ctxs[i], lens, seed=49 + i)
+                ctxs[i].track_weights()
+                qs.append(rows(len(lens), 1, 2 * G, d, 70 + i)[0])
+        for step in range(4):
+            for i, ctx in enumerate(ctxs):
+                with torch.cuda.stream(streams[i]):
+                    res = ctx.decode_attention(qs[i], accumulate=step % 2 == 0)
+                    if step == 3:
+                        got.append(res)
+        for i, ctx in enumerate(ctxs):
+            ctx.sync()
+            got[i] = [x.clone() for x in (*got[i], *(dense_weights(ctx, 0, max(sizes[i][0]))[r, :, :n] for r, n in enumerate(sizes[i][0])))]
+            torch.cuda.synchronize()
+            ctx.close()
+        if not together:
+            alone = got
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("cache", list(CACHES))
 def test_serving_loop(cache):
     """Steps, rounds and appends as a serving loop makes them: each step against the definition over the cache as it
@@ -390,6 +433,16 @@ def test_refusals():
         ctx.track_weights(torch.zeros((1, 2, 3, 16), device="cuda"))
     assert not w.any()
     ctx.close()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ctx = make([20], H=2, G=2, d=64, dtype=torch.bfloat16)
+        w = ctx.track_weights()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            w.add_(1)
+            assert status(ctx.track_weights, w) == KVC_ERR_STATE
+        side.synchronize()
+        ctx.close()
     wide = make([20], H=2, G=1, d=256, dtype=torch.bfloat16)
     assert status(wide.track_weights) == KVC_ERR_UNSUPPORTED
     wide.close()

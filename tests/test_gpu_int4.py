@@ -329,6 +329,31 @@ def test_a_broken_group_shows_only_where_it_is_read():
     ctx.close()
 
 
+def test_split_steps_with_empty_and_broken_requests():
+    """A few long requests (split over CTAs, merged by a second launch) beside an empty one, a short one and one with a
+    broken key group: its heads are NaN, the others' outputs are the definition's."""
+    lens = [20000, 0, 7, 4500]
+    ctx = make(lens, H=2, G=4)
+    fill(ctx, lens[:3], seed=92)
+    k, v = rows(4500, 1, 2, 128, 93), rows(4500, 1, 2, 128, 94)
+    k[0, 0, 4321, 1, 5] = float("nan")
+    ctx.append([3], k, v)
+    q = rows(4, 1, 8, 128, 18)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    assert torch.isnan(out[0, 3, 4:]).all() and torch.isnan(lse[0, 3, 4:]).all()
+    assert torch.isfinite(out[0, 3, :4]).all() and torch.isfinite(lse[0, 3, :4]).all()
+    assert not out[0, 1].any() and torch.isneginf(lse[0, 1]).all()
+    ctx2 = make(lens, H=2, G=4)
+    fill(ctx2, lens[:3], seed=92)
+    out2, lse2 = ctx2.decode_attention(q)
+    ctx2.sync()
+    assert torch.equal(out[0, :3], out2[0, :3]) and torch.equal(lse[0, :3], lse2[0, :3])
+    check_attention(ctx2, q, out2, lse2, [0], 128 ** -0.5)
+    ctx.close()
+    ctx2.close()
+
+
 @pytest.mark.parametrize("compaction", ["ordered", "hole_fill"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rounds_move_whole_rows(d, compaction):
