@@ -508,7 +508,11 @@ __global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D, bool ke
   }
   const bool none = !(l > 0.f) && !(keep_nan && isnan(l));
   p.out[head * D + c] = none ? 0.f : o / l;
-  if (p.lse && c == 0) p.lse[head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (c == 0) {
+    const float lse2 = none ? -INFINITY : m + log2f(l);
+    if (p.lse) p.lse[head] = lse2 * kLn2;
+    if (p.lse2) p.lse2[head] = lse2;
+  }
 }
 
 template <typename T, int D, int G>

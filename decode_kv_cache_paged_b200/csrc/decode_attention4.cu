@@ -663,58 +663,77 @@ int cluster_size(int64_t units, int np_max, int sms, int warps, size_t base_smem
   return cs;
 }
 
+// shared memory of the page slots
+template <int D, Mode4 MODE, int W, int ST>
+constexpr size_t kRing4 = 128 + (size_t)W * ST * kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
+
 template <int D, int GP, Mode4 MODE, int W, int ST>
 cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
   p.part_o = p.part_ml = nullptr;
-  const size_t slot = (size_t)kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 128 + W * ST * slot,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kRing4<D, MODE, W, ST>,
                              MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W, MODE != kWeights, s);
 }
 
-// A unit split over `splits` CTAs of 8 warps that are no cluster, and a launch
-// that merges them.
-template <int D, int GP>
+// A unit split over `splits` CTAs that are no cluster, and a launch that merges them.
+template <int D, int GP, int W>
 cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s) {
-  auto kernel = decode_attention4_kernel<D, GP, kStep, 8, 2>;
+  auto kernel = decode_attention4_kernel<D, GP, kStep, W, 2>;
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
-  const size_t smem = 128 + 8 * 2 * (size_t)Shape4<D>::kSlot;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = kRing4<D, kStep, W, 2>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   p.nsplit = splits;
   p.part_ml = p.part_o + (size_t)p.layer_count * p.R * p.hq * splits * D;
-  kernel<<<(unsigned)(units * splits), 256, smem, s>>>(p, G);
+  kernel<<<(unsigned)(units * splits), 32 * W, smem, s>>>(p, G);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_decode_attention_merge(p, D, true, s);
 }
 
-// Without weights and with units enough to give every warp slot of the GPU one
-// and a half, a unit is one warp's: no merge, and the start and end of a unit
-// cost a quarter of what four warps pay (2048 rows, 4096 units: 296 us against
-// 322; 1024 units: 105 against 91).
-// A few long requests are split without a cluster: the SMs take at most seven
-// clusters of 16 with a CTA each, so that clusters share SMs while others idle
-// (8 units of 32768 rows: 26 us against 36).
+// The step without weights.
+//   * With units enough to give every warp slot of the GPU one and a half, a
+//     unit is one warp's: no merge, and the start and end of a unit cost a
+//     quarter of what four warps pay (2048 rows, 4096 units: 296 us against
+//     322; 1024 units: 105 against 91).
+//   * A few long requests are split without a cluster: the SMs take at most
+//     seven clusters of 16 with a CTA each, so that clusters share SMs while
+//     others idle (8 units of 32768 rows: 26 us against 36).
+//   * So are units whose CTAs do not all fit at once: a cluster waits until
+//     places for all its CTAs are free together, and gives none back before its
+//     last CTA is done (512 units of 4096 to 32768 rows, 8 heads: 468 us against
+//     555, 4 heads: 372 against 409; 64 units of 16384 rows, 4 heads: 58 against
+//     72).  The merge launch costs more than that where they do fit (64 units of
+//     4096 rows: 25 against 23) or are only pairs (512 units of 4096 rows: 98
+//     against 95).
+//   The partials of a split must fit the workspace (p.max_splits), and no fewer
+//   than half the CTAs that the rule asks for will do.
+template <int D, int GP>
+cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
+  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
+  if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1, 2>(p, G, np_max, sms, s);
+  const int splits = std::min({p.max_splits, (np_max + 15) / 16, (int)(2LL * sms / units)});
+  if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
+  const int cs = cluster_size(units, np_max, sms, 4, kRing4<D, kStep, 4, 2>, 0);
+  const int parts = std::min(cs, p.max_splits);
+  if (parts >= 4 && 2 * parts > cs && units * parts > (GP == 8 ? 3LL : 4LL) * sms) return launch4_split<D, GP, 4>(p, G, parts, s);
+  return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
+}
+
 // With weights the scores stay in shared memory unless a CTA of the largest
 // cluster would have to keep more than 36 KB of them (more than 18432 rows at 8
 // heads): then too few warps fit an SM, and the weights take a launch of their
 // own that reads the keys again (64 requests of 4096 to 32768 rows, 8 heads:
-// 800 us against 1019; 4 heads, 32 KB each: 39 us against 54 for one request in
-// one launch, 625 against 619 for the 64).
+// 718 us against 1019; one of 32768: 48 against 62; 4 heads, 32 KB each: 46
+// against 38 for one request, 271 against 264 for 16, 585 against 626 for the
+// ragged 64).
 template <int D, int GP>
 cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
-  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
-  if (!p.weights) {
-    if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1, 2>(p, G, np_max, sms, s);
-    const int splits = std::min({p.max_splits, (np_max + 15) / 16, (int)(2LL * sms / units)});
-    if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP>(p, G, splits, s);
-    return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
-  }
+  if (!p.weights) return launch4_step<D, GP>(p, G, np_max, sms, s);
   if (!p.lse2 || (size_t)kPage * G * 4 * ((np_max + 15) / 16) <= 36 * 1024)
     return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
-  if (cudaError_t e = launch4_w<D, GP, kStep, 4, 2>(step, G, np_max, sms, s)) return e;
+  if (cudaError_t e = launch4_step<D, GP>(step, G, np_max, sms, s)) return e;
   return launch4_w<D, GP, kWeights, 4, 2>(p, G, np_max, sms, s);
 }
 

@@ -951,9 +951,10 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   p.qscale = (scale > 0.f ? scale : 1.0f / std::sqrt((float)c.head_dim)) * 1.4426950408889634f;
   p.weights = o.accumulate ? ctx->weights : nullptr;
   p.decay = o.decay;
-  p.max_splits = kAttnSplits / layer_count;
-  // scratch of the partials region; a layer's share of it holds d + 2 times 16 floats per query head
-  p.lse2 = o.accumulate && layer_count <= (c.head_dim + 2) * kAttnSplits ? ctx->d_attn : nullptr;
+  p.max_splits = (kAttnSplits - o.accumulate) / layer_count;
+  // the last floats of the partials region, past the partials of max_splits splits
+  const size_t heads = (size_t)R * c.num_q_heads, lse2_at = heads * ((size_t)(c.head_dim + 2) * kAttnSplits - layer_count);
+  p.lse2 = o.accumulate && layer_count <= c.head_dim + 2 ? ctx->d_attn + lse2_at : nullptr;
   if (ms_out) KVC_CUDA(ctx, cudaEventRecord(ctx->ev[0], ctx->stream));
   int launches = 0;
   cudaError_t e;

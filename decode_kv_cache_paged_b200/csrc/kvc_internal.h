@@ -71,7 +71,7 @@ struct DecodeAttnParams {
   float *weights;              // accumulated attention weights, indexed like the position map, or null
   float decay;                 // weights <- decay * weights + this step's
   int32_t max_splits;          // splits of a unit that part_o and part_ml have room for
-  float *lse2;                 // scratch [layer_count][R][Hq]: log2-sum-exp2 for a weights launch of its own, or null
+  float *lse2;                 // scratch [layer_count][R][Hq]: log2-sum-exp2 for a weights launch of its own, or null (apart from part_o, part_ml)
 };
 
 // Beacon update over the query ring.

@@ -79,7 +79,7 @@ def test_steps_accumulate(cache, d, G):
 
 @pytest.mark.parametrize("cache,G,lens", [("bf16", 4, [9001, 40, 700]), ("int4", 8, [32768, 3]), ("f32", 8, [32768]),
                                           ("bf16", 8, [32768]), ("int4", 4, [2048] * 20), ("int4", 4, [32768, 20001]),
-                                          ("int4", 8, [20003, 17, 19000, 0])], ids=str)
+                                          ("int4", 8, [20003, 17, 19000, 0]), ("int4", 8, [20003, 17, 19000, 0] * 5)], ids=str)
 def test_long(cache, G, lens):
     ctx = make(lens, H=2, G=G, dtype=CACHES[cache])
     fill(ctx, lens, seed=5)

@@ -329,6 +329,19 @@ def test_a_broken_group_shows_only_where_it_is_read():
     ctx.close()
 
 
+@pytest.mark.parametrize("G,layers,lens", [(8, 1, [9000, 0, 1, 16, 4097, 300, 8999, 5000]), (4, 2, [9001, 33, 0, 7000, 5000, 8000, 2, 9000]),
+                                           (8, 3, [5000, 4999, 17, 0])])
+def test_attention_more_ctas_than_fit(G, layers, lens):
+    """Units split over more CTAs than fit the GPU at once, their partials merged by a second launch."""
+    ctx = make(lens, layers=layers, H=8, G=G)
+    fill(ctx, lens, seed=95)
+    q = rows(len(lens), layers, 8 * G, 128, 19)[0]
+    out, lse = ctx.decode_attention(q)
+    ctx.sync()
+    print(check_attention(ctx, q, out, lse, range(layers), 128 ** -0.5))
+    ctx.close()
+
+
 def test_split_steps_with_empty_and_broken_requests():
     """A few long requests (split over CTAs, merged by a second launch) beside an empty one, a short one and one with a
     broken key group: its heads are NaN, the others' outputs are the definition's."""
