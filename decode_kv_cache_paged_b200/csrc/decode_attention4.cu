@@ -26,9 +26,9 @@
 //     scaled per head to |q| < 2048 and split into an integer and the rest, both
 //     fp16: the integers' products and sums are exact (the tensor cores
 //     truncate each product to the place of the largest, which costs 5e-6 of a
-//     score otherwise), those of the rest are too small to matter.  A group is
-//     a sum of its own, which s multiplies in fp32, where lo * the group's sum
-//     of q joins it.
+//     score otherwise); the rest's have columns of their own, or join the sum with
+//     a truncation the size of an fp32 rounding.  A group is a sum of its own,
+//     which s multiplies in fp32, where lo * the group's sum of q joins it.
 //     (8-bit floats would take fewer ands, but their products expand to fp16
 //     ones with a conversion per two codes: measured 24 instructions of the
 //     logic pipe more per page.)
@@ -322,10 +322,13 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
   [[maybe_unused]] float w_lse0 = 0.f, w_lse1 = 0.f;  // of columns 2t and 2t + 1
   if constexpr (MODE == kWeights) {
     const float *src = p.lse2 + ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
-    w_lse0 = 2 * t < G ? src[2 * t] : 0.f;
-    w_lse1 = 2 * t + 1 < G ? src[2 * t + 1] : 0.f;
+    w_lse0 = 2 * t < G ? src[2 * t] : INFINITY;  // columns of a repeated head add exp2(-inf)
+    w_lse1 = 2 * t + 1 < G ? src[2 * t + 1] : INFINITY;
   }
   const int v0 = 2 * t, v1 = ((2 * t + 4) & 7) + 8;  // P's rows 2t and 2t + 1; v0 + 1 and v1 + 1 are 2t + 8 and 2t + 9
+
+  [[maybe_unused]] float *const w_base = p.weights + ((int64_t)u.l * p.num_pages * p.hkv + u.h) * kPage + ra + (t & 1);
+  [[maybe_unused]] const int w_stride = p.hkv * kPage;
 
   float m0 = -INFINITY, m1 = -INFINITY;  // running maxima of columns 2t and 2t + 1 (base 2)
   float o[S::kTiles][4], e[4];  // e: the mid term (rows n), the sum of P (rows n + 8)
@@ -339,17 +342,13 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
   int k = 0;
   for (; k < n_my; ++k) {
     const int slot = k % kStages;
-    [[maybe_unused]] float2 w_old[kPair];
-    [[maybe_unused]] float *w_at[kPair];
-    if constexpr (MODE == kWeights) {  // lanes t = 0: the weights of rows ra and ra + 1, read ahead of the wait
-#pragma unroll
-      for (int y = 0; y < kPair; ++y) {
-        const int pg = first + k * kPair * kWarps + y;
-        w_at[y] = nullptr;
-        if (t == 0 && pg < u.pg1 && pg * kPage + ra < u.len) {
-          w_at[y] = p.weights + (((int64_t)u.l * p.num_pages + u.bt[pg]) * p.hkv + u.h) * kPage + ra;
-          w_old[y] = *reinterpret_cast<const float2 *>(w_at[y]);
-        }
+    [[maybe_unused]] float w_old = 0.f;
+    [[maybe_unused]] float *w_at = nullptr;
+    if constexpr (MODE == kWeights) {  // this lane's row (page t / 2, row ra + t % 2): its weight, read ahead of the wait
+      const int pg = first + k * kPair * kWarps + (t >> 1);
+      if (pg < u.pg1 && pg * kPage + ra + (t & 1) < u.len) {
+        w_at = w_base + (int64_t)u.bt[pg] * w_stride;
+        w_old = *w_at;
       }
     }
     const uint32_t parity = (uint32_t)((k / kStages) & 1);
@@ -402,16 +401,17 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
         const uint32_t a0 = a & 0x000f000fu, a1 = a & 0x00f000f0u, a2 = a >> 8 & 0x000f000fu, a3 = a >> 8 & 0x00f000f0u;
         const uint32_t b0 = b & 0x000f000fu, b1 = b & 0x00f000f0u, b2 = b >> 8 & 0x000f000fu, b3 = b >> 8 & 0x00f000f0u;
         const float sa = __uint_as_float(ga[gr] & 0xfff00000u), sb = __uint_as_float(gb[gr] & 0xfff00000u);
-#pragma unroll
-        for (int z = 0; z < kQt; ++z) {
-          float d[4];
-          mma16816h_zero(d, a0, b0, a1, b1, qb[z][2 * gr][0], qb[z][2 * gr][1]);
-          mma16816h(d, a2, b2, a3, b3, qb[z][2 * gr + 1][0], qb[z][2 * gr + 1][1]);
-          acc[0] = fmaf(sa, d[0], acc[0]);
-          acc[1] = fmaf(sa, d[1], acc[1]);
-          acc[2] = fmaf(sb, d[2], acc[2]);
-          acc[3] = fmaf(sb, d[3], acc[3]);
+        float d[4];
+        mma16816h_zero(d, a0, b0, a1, b1, qb[0][2 * gr][0], qb[0][2 * gr][1]);
+        mma16816h(d, a2, b2, a3, b3, qb[0][2 * gr + 1][0], qb[0][2 * gr + 1][1]);
+        if constexpr (kQt == 2) {
+          mma16816h(d, a0, b0, a1, b1, qb[kQt - 1][2 * gr][0], qb[kQt - 1][2 * gr][1]);
+          mma16816h(d, a2, b2, a3, b3, qb[kQt - 1][2 * gr + 1][0], qb[kQt - 1][2 * gr + 1][1]);
         }
+        acc[0] = fmaf(sa, d[0], acc[0]);
+        acc[1] = fmaf(sa, d[1], acc[1]);
+        acc[2] = fmaf(sb, d[2], acc[2]);
+        acc[3] = fmaf(sb, d[3], acc[3]);
       }
       s[y][0] = acc[0] * lam0;
       s[y][1] = acc[1] * lam1;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[y][x] += __shfl_xor_sync(0xffffffffu, s[y][x], 2);
     }
-    if (valid < kPair * kPage) {
+    if (MODE != kWeights && valid < kPair * kPage) {
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
         if (y * kPage + ra >= valid) s[y][0] = s[y][1] = -INFINITY;
@@ -429,25 +429,19 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
       }
     }
     if constexpr (MODE == kWeights) {
+      static_assert(kPair == 2);
+      // sums over this lane's two columns, then over the four lanes of a row, each left with one row
+      float a[kPair], b[kPair];
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
-        // lanes t and t ^ 2 hold the same heads where GP = 4; a repeated head counts once
-        const bool c0 = 2 * t < G, c1 = 2 * t + 1 < G;
-        float a = (c0 ? attn_ex2(s[y][0] - w_lse0) : 0.f) + (c1 ? attn_ex2(s[y][1] - w_lse1) : 0.f);
-        float b = (c0 ? attn_ex2(s[y][2] - w_lse0) : 0.f) + (c1 ? attn_ex2(s[y][3] - w_lse1) : 0.f);
-        a += __shfl_xor_sync(0xffffffffu, a, 1);
-        b += __shfl_xor_sync(0xffffffffu, b, 1);
-        a += __shfl_xor_sync(0xffffffffu, a, 2);
-        b += __shfl_xor_sync(0xffffffffu, b, 2);
-        if (w_at[y]) {
-          a = fmaf(p.decay, w_old[y].x, a);
-          b = fmaf(p.decay, w_old[y].y, b);
-          if (y * kPage + ra + 1 < valid)
-            *reinterpret_cast<float2 *>(w_at[y]) = make_float2(a, b);
-          else  // the last row: what lies past it stays
-            *w_at[y] = a;
-        }
+        a[y] = attn_ex2(s[y][0] - w_lse0) + attn_ex2(s[y][1] - w_lse1);
+        b[y] = attn_ex2(s[y][2] - w_lse0) + attn_ex2(s[y][3] - w_lse1);
       }
+      const bool hi = t & 2, odd = t & 1;
+      float x = (hi ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[1], 2);
+      float z = (hi ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, hi ? b[0] : b[1], 2);
+      x = (odd ? z : x) + __shfl_xor_sync(0xffffffffu, odd ? x : z, 1);
+      if (w_at) *w_at = fmaf(p.decay, w_old, x);
       __syncwarp();  // every lane has read the slot
       if (k + kStages < n_my) issue_pair(k + kStages);
       continue;
@@ -700,7 +694,7 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
 //     others idle (8 units of 32768 rows: 26 us against 36).
 //   * So are units whose CTAs do not all fit at once: a cluster waits until
 //     places for all its CTAs are free together, and gives none back before its
-//     last CTA is done (512 units of 4096 to 32768 rows, 8 heads: 468 us against
+//     last CTA is done (512 units of 4096 to 32768 rows, 8 heads: 452 us against
 //     555, 4 heads: 372 against 409; 64 units of 16384 rows, 4 heads: 58 against
 //     72).  The merge launch costs more than that where they do fit (64 units of
 //     4096 rows: 25 against 23) or are only pairs (512 units of 4096 rows: 98
@@ -720,17 +714,20 @@ cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, 
 }
 
 // With weights the scores stay in shared memory unless a CTA of the largest
-// cluster would have to keep more than 36 KB of them (more than 18432 rows at 8
-// heads): then too few warps fit an SM, and the weights take a launch of their
-// own that reads the keys again (64 requests of 4096 to 32768 rows, 8 heads:
-// 718 us against 1019; one of 32768: 48 against 62; 4 heads, 32 KB each: 46
-// against 38 for one request, 271 against 264 for 16, 585 against 626 for the
-// ragged 64).
+// cluster would have to keep more than 36 KB of them, or 20 KB where units
+// abound (18432 and 10240 rows at 8 heads): then too few warps fit an SM, and
+// the weights take a launch of their own that reads the keys again.  Us in one
+// launch and in two: 8 heads, 512 units of 12288 rows 507, 430, of 8192 rows
+// 311, 302, of 4096 to 32768 rows 1019, 644; 8 units of 32768 rows 62, 44, of
+// 12288 rows 23, 25.  4 heads, 512 units of 24576 rows 794, 697, of 16384 rows
+// 494, 474; 32 ragged units up to 32768 rows 50, 63; 2 heads, 512 units of 32768
+// rows 851, 902.
 template <int D, int GP>
 cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
   if (!p.weights) return launch4_step<D, GP>(p, G, np_max, sms, s);
-  if (!p.lse2 || (size_t)kPage * G * 4 * ((np_max + 15) / 16) <= 36 * 1024)
-    return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
+  const size_t keep = (size_t)kPage * G * 4 * ((np_max + 15) / 16);
+  const size_t most = (int64_t)p.layer_count * p.R * p.hkv >= 128 ? 20 * 1024 : 36 * 1024;
+  if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
   if (cudaError_t e = launch4_step<D, GP>(step, G, np_max, sms, s)) return e;

@@ -79,12 +79,25 @@ def test_steps_accumulate(cache, d, G):
 
 @pytest.mark.parametrize("cache,G,lens", [("bf16", 4, [9001, 40, 700]), ("int4", 8, [32768, 3]), ("f32", 8, [32768]),
                                           ("bf16", 8, [32768]), ("int4", 4, [2048] * 20), ("int4", 4, [32768, 20001]),
-                                          ("int4", 8, [20003, 17, 19000, 0]), ("int4", 8, [20003, 17, 19000, 0] * 5)], ids=str)
+                                          ("int4", 8, [20003, 17, 19000, 0]), ("int4", 8, [20003, 17, 19000, 0] * 5),
+                                          ("int4", 2, [32768] + [5, 0, 2047, 2048, 31] * 13)], ids=str)
 def test_long(cache, G, lens):
     ctx = make(lens, H=2, G=G, dtype=CACHES[cache])
     fill(ctx, lens, seed=5)
     ctx.track_weights()
     run_step(ctx, rows(len(lens), 1, 2 * G, 128, 6, dtype=ctx.dtype)[0], [0])
+    ctx.close()
+
+
+@pytest.mark.parametrize("G,d,H", [(8, 64, 2), (8, 128, 1), (4, 64, 32)])
+def test_long_layers(G, d, H):
+    """Weights by a launch of their own, two layers of three in a call."""
+    lens = [20501, 0, 33]
+    ctx = make(lens, layers=3, H=H, G=G, d=d)
+    fill(ctx, lens, seed=6)
+    w = ctx.track_weights()
+    w.uniform_()
+    run_step(ctx, rows(len(lens), 2, H * G, d, 7)[0], [1, 2], decay=0.5)
     ctx.close()
 
 
