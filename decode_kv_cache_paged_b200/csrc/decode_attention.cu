@@ -529,7 +529,7 @@ template <typename T, int D, int G>
 cudaError_t launch_acc(DecodeAttnParams p, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention_kernel<T, D, G, true>;
   p.part_o = p.part_ml = nullptr;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, AttnShape<T, D, G>::kSmem,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 3, AttnShape<T, D, G>::kSmem,
                              (size_t)kPage * G * 4, kThreads, true, s);
 }
 

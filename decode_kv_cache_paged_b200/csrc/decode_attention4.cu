@@ -53,6 +53,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "attn_cluster.cuh"
 #include "int4.cuh"
@@ -60,7 +61,6 @@
 namespace kvc {
 namespace {
 
-constexpr size_t kSmemHalf = 111 * 1024;        // dynamic shared memory with which two CTAs fit an SM
 constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // the most for one, less the static shared memory
 constexpr int kPair = 2;    // pages per slot
 
@@ -149,9 +149,12 @@ constexpr float kLazy = 8.f;  // a score may exceed the running maximum by this 
 enum Mode4 { kStep, kStepWeights, kWeights };
 
 // GP: columns of the product that hold query heads, 4 (G <= 4: the second parts
-// take the other four) or 8.  W: warps of a CTA; 16 warps fit an SM.
+// take the other four) or 8.  W: warps of a CTA.
+template <int GP, Mode4 MODE, int W>
+constexpr int kFit4 = (GP == 8 && MODE != kWeights ? 12 : 16) / W;  // CTAs whose registers fit an SM
+
 template <int D, int GP, Mode4 MODE, int W, int ST>
-__global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16) / W) decode_attention4_kernel(DecodeAttnParams p, int G) {
+__global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_kernel(DecodeAttnParams p, int G) {
   using S = Shape4<D>;
   constexpr int kWarps = W, kThreads = 32 * W, kStages = ST;
   constexpr bool kValues = MODE != kWeights;
@@ -630,31 +633,39 @@ __global__ void __launch_bounds__(32 * W, (GP == 8 && MODE != kWeights ? 12 : 16
   attn_finish<D, kWarps, kThreads>(p, u, G, red, m_s, l_s, mg, MODE == kStepWeights ? scores : nullptr);
 }
 
-// Cluster size: CTAs that share a unit, a power of two up to 16.  It grows
-//   * until a CTA's scores leave room for a second CTA on the SM (page_smem
-//     bytes a page, 0 without weights), or only fit at all where the page slots
-//     alone take half of it (fp32 rows of 128 channels);
-//   * while the units are fewer than 1.5 CTAs per SM and every warp would keep
-//     two pages, or fewer than 4 and a CTA's share more than 64 pages;
-//   * until a CTA's share is at most 256 pages, so that requests of different
-//     lengths end together.
-// Measured for 4 warps a CTA (us; us at half and at twice the size): bf16 with
-// weights, 2048 units of 2048 rows: 1 CTA 347 (-, 408); 32 units of up to 8191
-// rows: 8 CTAs 29 (44, 34).  4 bits, 512 units of 4096 to 32768 rows, 8 heads:
-// 8 CTAs 563 (595, -); with weights and 4 heads 622 (891, 675); 64 units of 8192
-// rows: 8 CTAs 33 (36, -).
-int cluster_size(int64_t units, int np_max, int sms, int warps, size_t base_smem, size_t page_smem) {
-  const size_t room = base_smem + 16 * 1024 > kSmemHalf ? kMaxSmem : kSmemHalf;
-  int cs = 1;
-  while (cs < 16) {
+// Cluster size: CTAs that share a unit, a power of two up to 16, so that every
+// warp keeps more than a page and a CTA at most 256 (requests of different
+// lengths then end together).  Of those the one with the least estimated time:
+//   waves * (pages of a CTA + kFixed) * a / rate(a),
+// a the CTAs that share an SM (at most what its shared memory, page_smem bytes
+// a page with weights, and `fit` allow) and rate(a) = 1 - 2^(-warps / 4) how near
+// their warps bring it to its full rate; a last wave that is not full counts
+// for three quarters of a full one more.  kFixed is a CTA's start and end in
+// pages.
+// Measured for 4 warps a CTA (us at 1, 2, 4, 8, 16 CTAs): 4 bits with weights, 4
+// heads, 64 units of 8192 rows 97, 54, *39, 48; 256 units of 4096 rows *67, 74, 77,
+// 78; 4096 units of 2048 rows *380, 456, 514; 8 heads, 160 units of 3000 rows 85,
+// 61, *49, 62; without weights, 4 heads, 64 units of 8192 rows 91, 52, *36, 33; 512
+// units of 2048 rows *54, 62, 66; bf16 with weights, 32 units of 16384 rows -, 154,
+// 82, *58, 83 (* the rule's).
+int cluster_size(int64_t units, int np_max, int sms, int warps, int fit, size_t base_smem, size_t page_smem) {
+  constexpr double kFixed = 48;
+  constexpr size_t kSm = 228 * 1024, kCta = 1024 + 2304;  // shared memory of an SM; a CTA's beside the dynamic
+  int best = 16;
+  double least = 1e300;
+  for (int cs = 1; cs <= 16; cs *= 2) {
+    if (cs > 1 && (np_max + cs / 2 - 1) / (cs / 2) <= 2 * warps) break;
     const int share = (np_max + cs - 1) / cs;
-    const int64_t ctas = units * cs;
-    if (!(base_smem + page_smem * share > room || (2 * ctas < 3LL * sms && share > 2 * warps) ||
-          (ctas < 4LL * sms && share > 64) || share > 256))
-      break;
-    cs *= 2;
+    const size_t smem = base_smem + page_smem * share;
+    if (smem > kMaxSmem || (share > 256 && cs < 16)) continue;
+    const int slots = std::max(1, std::min(fit, (int)(kSm / (smem + kCta))));
+    const double ctas = (double)units * cs, waves = ctas / ((double)sms * slots);
+    const int a = std::min<int64_t>(slots, (units * cs + sms - 1) / sms);
+    const double cost = (waves <= 1 ? 1 : 0.25 * waves + 0.75 * std::ceil(waves)) * (share + kFixed) * a /
+                        (1 - std::exp2(-a * warps / 4.0));
+    if (cost < least) least = cost, best = cs;
   }
-  return cs;
+  return best;
 }
 
 // shared memory of the page slots
@@ -665,7 +676,7 @@ template <int D, int GP, Mode4 MODE, int W, int ST>
 cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
   p.part_o = p.part_ml = nullptr;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kRing4<D, MODE, W, ST>,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kFit4<GP, MODE, W>, kRing4<D, MODE, W, ST>,
                              MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W, MODE != kWeights, s);
 }
 
@@ -707,9 +718,9 @@ cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, 
   if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1, 2>(p, G, np_max, sms, s);
   const int splits = std::min({p.max_splits, (np_max + 15) / 16, (int)(2LL * sms / units)});
   if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
-  const int cs = cluster_size(units, np_max, sms, 4, kRing4<D, kStep, 4, 2>, 0);
+  const int cs = cluster_size(units, np_max, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4, 2>, 0);
   const int parts = std::min(cs, p.max_splits);
-  if (parts >= 4 && 2 * parts > cs && units * parts > (GP == 8 ? 3LL : 4LL) * sms) return launch4_split<D, GP, 4>(p, G, parts, s);
+  if (parts >= 4 && 2 * parts > cs && units * parts > (int64_t)kFit4<GP, kStep, 4> * sms) return launch4_split<D, GP, 4>(p, G, parts, s);
   return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
 }
 
@@ -736,11 +747,11 @@ cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaS
 
 }  // namespace
 
-cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
-                                size_t page_smem, int threads, bool cluster, cudaStream_t s) {
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, int fit,
+                                size_t base_smem, size_t page_smem, int threads, bool cluster, cudaStream_t s) {
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (units <= 0) return cudaSuccess;
-  const int cs = cluster_size(units, np_max, sms, threads / 32, base_smem, page_smem);
+  const int cs = cluster_size(units, np_max, sms, threads / 32, fit, base_smem, page_smem);
   const size_t smem = base_smem + page_smem * ((np_max + cs - 1) / cs);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e;

@@ -140,11 +140,12 @@ cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int
 // weights over the other caches.  np_max: most pages a request may have when
 // the launch runs; sms: the device's SMs.
 // launch_attn_cluster picks how many CTAs share a unit and launches `kernel`
-// with (DecodeAttnParams, int G): base_smem is its shared memory without the
-// scores, page_smem the bytes of scores per page (0 without weights), cluster
-// whether the CTAs of a unit are a cluster.
-cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, size_t base_smem,
-                                size_t page_smem, int threads, bool cluster, cudaStream_t s);
+// with (DecodeAttnParams, int G): fit is how many CTAs an SM's registers hold,
+// base_smem the kernel's shared memory without the scores, page_smem the bytes
+// of scores per page (0 without weights), cluster whether the CTAs of a unit
+// are a cluster.
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, int fit,
+                                size_t base_smem, size_t page_smem, int threads, bool cluster, cudaStream_t s);
 cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
                                      cudaStream_t s);
 cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, int np_max, int sms,
