@@ -26,8 +26,8 @@
 //     scaled per head to |q| < 2048 and split into an integer and the rest, both
 //     fp16: the integers' products and sums are exact (the tensor cores
 //     truncate each product to the place of the largest, which costs 5e-6 of a
-//     score otherwise); the rest's have columns of their own, or join the sum with
-//     a truncation the size of an fp32 rounding.  A group is a sum of its own,
+//     score otherwise); the rest's have columns of their own, or join the sum (8
+//     heads) with a truncation the size of an fp32 rounding.  A group is a sum of its own,
 //     which s multiplies in fp32, where lo * the group's sum of q joins it.
 //     (8-bit floats would take fewer ands, but their products expand to fp16
 //     ones with a conversion per two codes: measured 24 instructions of the
@@ -40,9 +40,11 @@
 //     gives the softmax's sum.
 //   * P enters as three bf16 terms, all of its 24 bits: two would leave 2^-17 of
 //     a weight, 1.2e-6 of an output where fp32 sums leave 3e-7.
-//   * With at most 4 query heads per KV head the two parts of q, and the first
-//     two terms of P, are columns 0..3 and 4..7 of one product, and the third
-//     term takes another; with 8 heads each takes one.
+//   * With at most 4 query heads per KV head the two parts of a head's query, and
+//     the first two terms of its P, are neighbouring columns of one product, which
+//     one lane holds: no lane repeats another's softmax, and a head's sums are one.
+//     P's third term takes another product; with 8 heads each part and term takes
+//     one.
 //   * The running maximum is lazy: two pages' scores are compared with it and
 //     the sums are rescaled only when one exceeds it by more than 2^8, so a
 //     page needs no reduction across lanes.
@@ -148,8 +150,7 @@ constexpr float kLazy = 8.f;  // a score may exceed the running maximum by this 
 // log-sum-exp (p.lse2), for rows too many to keep the scores of.
 enum Mode4 { kStep, kStepWeights, kWeights };
 
-// GP: columns of the product that hold query heads, 4 (G <= 4: the second parts
-// take the other four) or 8.  W: warps of a CTA.
+// GP: query heads that a product's 8 columns hold, 4 (G <= 4: two columns each) or 8.  W: warps of a CTA.
 template <int GP, Mode4 MODE, int W>
 constexpr int kFit4 = (GP == 8 && MODE != kWeights ? 12 : 16) / W;  // CTAs whose registers fit an SM
 
@@ -217,20 +218,19 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
   };
   for (int k = 0; k < min(n_my, kStages); ++k) issue_pair(k);
 
-  // query fragments.  Column n: head n & 3, its integers in columns 0..3 and the
-  // rest in 4..7 (GP = 4), or head n with the two parts in two tiles (GP = 8); a
-  // smaller group repeats.  Products 2 gr and 2 gr + 1 are group gr's, with this
-  // lane's unit t of it: low nibbles first, then high ones (times 2^-4: their
-  // codes are 2^4 larger).
+  // query fragments.  Column n: GP = 4: head n / 2, its integers in even columns
+  // and the rest in odd ones, so that a lane's two columns are one head; GP = 8:
+  // head n, the two parts in two tiles.  A smaller group repeats.  Products 2 gr
+  // and 2 gr + 1 are group gr's, with this lane's unit t of it: low nibbles
+  // first, then high ones (times 2^-4: their codes are 2^4 larger).
   constexpr int kQt = GP == 4 ? 1 : 2;
+  constexpr int C = GP == 4 ? 1 : 2;  // heads of this lane: head t, or 2 t and 2 t + 1
+  const int head_of_lane = C * t;
   uint32_t qb[kQt][2 * kInt4Groups][2];
-  // sums of q beside lo, columns 2t and 2t + 1.  GP = 4: lanes t and t ^ 2 hold
-  // the same heads and are added later, so each takes two groups, from 2 (t / 2).
-  constexpr int kLo = GP == 4 ? 2 : kInt4Groups;
-  float qsum[kLo][2];
-  float lam0, lam1;  // from a column's sum to base-2 scores, columns 2t and 2t + 1
+  float qsum[kInt4Groups][C];  // sums of q beside lo
+  float lam[C];                // from a head's sum to base-2 scores
   {
-    const int g = (GP == 4 ? n & 3 : n) % G;
+    const int g = (GP == 4 ? n >> 1 : n) % G;
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) +
                         ((((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G + g) * D + t * (D / 16));
     float x[kInt4Groups][D / 16], top = 0.f, bad = 0.f, sum[kInt4Groups];
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
       for (int z = 0; z < kQt; ++z) {
         float c[D / 16];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) c[i] = (GP == 4 ? n >= 4 : z == 1) ? part[1][i] : part[0][i];
+        for (int i = 0; i < D / 16; ++i) c[i] = (GP == 4 ? n & 1 : z) ? part[1][i] : part[0][i];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           if constexpr (D == 128) {  // codes i and i + 4 of a word share a register
@@ -301,46 +301,53 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
       sum[gr] *= 0x1p-24f;  // the codes' unit
     }
     // column c's values sit with lanes n = c
+    const float lam_n = p.qscale * 0x1p24f * __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-    for (int i = 0; i < kLo; ++i)
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float a = __shfl_sync(0xffffffffu, sum[i], (2 * t + x) * 4);
-        if constexpr (GP == 4) {
-          const float b = __shfl_sync(0xffffffffu, sum[i + 2], (2 * t + x) * 4);
-          qsum[i][x] = t >= 2 ? b : a;
-        } else {
-          qsum[i][x] = a;
-        }
-      }
-    const float lam = p.qscale * 0x1p24f * __uint_as_float((uint32_t)(127 - ex) << 23);
-    lam0 = __shfl_sync(0xffffffffu, lam, (2 * t) * 4);
-    lam1 = __shfl_sync(0xffffffffu, lam, (2 * t + 1) * 4);
+      for (int i = 0; i < kInt4Groups; ++i) qsum[i][c] = __shfl_sync(0xffffffffu, sum[i], (2 * t + c) * 4);
+      lam[c] = __shfl_sync(0xffffffffu, lam_n, (2 * t + c) * 4);
+    }
   }
 
   constexpr int kPt = GP == 4 ? 2 : 3;  // products for the terms of P
   // rows of a page: fragment rows n and n + 8 are page rows ra and ra + 1, an
   // order in which no two lanes of a shared-memory phase meet in a bank
   const int ra = (n & 1) ? ((n + 3) & 7) + 8 : n;
-  [[maybe_unused]] float w_lse0 = 0.f, w_lse1 = 0.f;  // of columns 2t and 2t + 1
+  [[maybe_unused]] float w_lse[C];
   if constexpr (MODE == kWeights) {
     const float *src = p.lse2 + ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
-    w_lse0 = 2 * t < G ? src[2 * t] : INFINITY;  // columns of a repeated head add exp2(-inf)
-    w_lse1 = 2 * t + 1 < G ? src[2 * t + 1] : INFINITY;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      w_lse[c] = head_of_lane + c < G ? src[head_of_lane + c] : INFINITY;  // a repeated head adds exp2(-inf)
   }
   const int v0 = 2 * t, v1 = ((2 * t + 4) & 7) + 8;  // P's rows 2t and 2t + 1; v0 + 1 and v1 + 1 are 2t + 8 and 2t + 9
 
   [[maybe_unused]] float *const w_base = p.weights + ((int64_t)u.l * p.num_pages * p.hkv + u.h) * kPage + ra + (t & 1);
   [[maybe_unused]] const int w_stride = p.hkv * kPage;
 
-  float m0 = -INFINITY, m1 = -INFINITY;  // running maxima of columns 2t and 2t + 1 (base 2)
-  float o[S::kTiles][4], e[4];  // e: the mid term (rows n), the sum of P (rows n + 8)
+  float m[C];  // running maxima (base 2)
+  float o[S::kTiles][2 * C], e[2 * C];  // [x C + c]: fragment rows n + 8 x; e: the mid term (x = 0), the sum of P
+#pragma unroll
+  for (int c = 0; c < C; ++c) m[c] = -INFINITY;
 #pragma unroll
   for (int i = 0; i < S::kTiles; ++i)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+    for (int x = 0; x < 2 * C; ++x) o[i][x] = 0.f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) e[x] = 0.f;
+  for (int x = 0; x < 2 * C; ++x) e[x] = 0.f;
+  // adds a product to a sum; GP = 4: the columns of P's first and second terms together
+  auto add_tile = [](float (&sum)[2 * C], const float (&d)[4]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if constexpr (C == 1) {
+        sum[x] += d[2 * x] + d[2 * x + 1];
+      } else {
+        sum[x * C] += d[2 * x];
+        sum[x * C + C - 1] += d[2 * x + 1];
+      }
+    }
+  };
 
   int k = 0;
   for (; k < n_my; ++k) {
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
     const uint8_t *base = ring + slot * kSlot;
     const int valid = rows_end - (first + k * kPair * kWarps) * kPage;  // rows here; what lies past them is anything
 
-    // 1. base-2 scores: s[y][0..1] of page row ra, [2..3] of row ra + 1, for columns 2t, 2t + 1
-    float s[kPair][4];
+    // 1. base-2 scores s[y][x C + c] of page row ra + x
+    float s[kPair][2 * C];
 #pragma unroll
     for (int y = 0; y < kPair; ++y) {
       const uint8_t *row0 = base + y * kYStride + ra * S::kRow, *row1 = row0 + S::kRow;
@@ -380,23 +387,16 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
         wa[0] = a.x, wa[1] = a.y;
         wb[0] = b.x, wb[1] = b.y;
       }
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float acc[2 * C];
       // lo by the sums of q
-      uint32_t ka[kLo], kb[kLo];
-      if constexpr (GP == 4) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(row0 + (t >> 1) * 8);
-        const uint2 b = *reinterpret_cast<const uint2 *>(row1 + (t >> 1) * 8);
-        ka[0] = a.x, ka[1] = a.y, kb[0] = b.x, kb[1] = b.y;
-      } else {
 #pragma unroll
-        for (int i = 0; i < kLo; ++i) ka[i] = ga[i], kb[i] = gb[i];
-      }
+      for (int c = 0; c < C; ++c) {
+        acc[c] = acc[C + c] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kLo; ++i) {
-        acc[0] = fmaf(bf16_lo(ka[i]), qsum[i][0], acc[0]);
-        acc[1] = fmaf(bf16_lo(ka[i]), qsum[i][1], acc[1]);
-        acc[2] = fmaf(bf16_lo(kb[i]), qsum[i][0], acc[2]);
-        acc[3] = fmaf(bf16_lo(kb[i]), qsum[i][1], acc[3]);
+        for (int i = 0; i < kInt4Groups; ++i) {
+          acc[c] = fmaf(bf16_lo(ga[i]), qsum[i][c], acc[c]);
+          acc[C + c] = fmaf(bf16_lo(gb[i]), qsum[i][c], acc[C + c]);
+        }
       }
 #pragma unroll
       for (int gr = 0; gr < kInt4Groups; ++gr) {
@@ -411,34 +411,44 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
           mma16816h(d, a0, b0, a1, b1, qb[kQt - 1][2 * gr][0], qb[kQt - 1][2 * gr][1]);
           mma16816h(d, a2, b2, a3, b3, qb[kQt - 1][2 * gr + 1][0], qb[kQt - 1][2 * gr + 1][1]);
         }
-        acc[0] = fmaf(sa, d[0], acc[0]);
-        acc[1] = fmaf(sa, d[1], acc[1]);
-        acc[2] = fmaf(sb, d[2], acc[2]);
-        acc[3] = fmaf(sb, d[3], acc[3]);
+        if constexpr (C == 1) {  // the columns of the head's two parts
+          acc[0] = fmaf(sa, d[1], fmaf(sa, d[0], acc[0]));
+          acc[1] = fmaf(sb, d[3], fmaf(sb, d[2], acc[1]));
+        } else {
+          acc[0] = fmaf(sa, d[0], acc[0]);
+          acc[C - 1] = fmaf(sa, d[1], acc[C - 1]);
+          acc[C] = fmaf(sb, d[2], acc[C]);
+          acc[2 * C - 1] = fmaf(sb, d[3], acc[2 * C - 1]);
+        }
       }
-      s[y][0] = acc[0] * lam0;
-      s[y][1] = acc[1] * lam1;
-      s[y][2] = acc[2] * lam0;
-      s[y][3] = acc[3] * lam1;
-      if constexpr (GP == 4)  // the columns with the other part
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[y][x] += __shfl_xor_sync(0xffffffffu, s[y][x], 2);
+      for (int c = 0; c < C; ++c) {
+        s[y][c] = acc[c] * lam[c];
+        s[y][C + c] = acc[C + c] * lam[c];
+      }
     }
     if (MODE != kWeights && valid < kPair * kPage) {
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
-        if (y * kPage + ra >= valid) s[y][0] = s[y][1] = -INFINITY;
-        if (y * kPage + ra + 1 >= valid) s[y][2] = s[y][3] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (y * kPage + ra >= valid) s[y][c] = -INFINITY;
+          if (y * kPage + ra + 1 >= valid) s[y][C + c] = -INFINITY;
+        }
       }
     }
     if constexpr (MODE == kWeights) {
       static_assert(kPair == 2);
-      // sums over this lane's two columns, then over the four lanes of a row, each left with one row
+      // sums over this lane's heads, then over the four lanes of a row, each left with one row
       float a[kPair], b[kPair];
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
-        a[y] = attn_ex2(s[y][0] - w_lse0) + attn_ex2(s[y][1] - w_lse1);
-        b[y] = attn_ex2(s[y][2] - w_lse0) + attn_ex2(s[y][3] - w_lse1);
+        a[y] = attn_ex2(s[y][0] - w_lse[0]);
+        b[y] = attn_ex2(s[y][C] - w_lse[0]);
+        if constexpr (C == 2) {
+          a[y] += attn_ex2(s[y][C - 1] - w_lse[C - 1]);
+          b[y] += attn_ex2(s[y][2 * C - 1] - w_lse[C - 1]);
+        }
       }
       const bool hi = t & 2, odd = t & 1;
       float x = (hi ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[1], 2);
@@ -454,61 +464,68 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
       for (int y = 0; y < kPair; ++y) {
         // the buffer holds whole pages: the second page of the last pair may lie past it
         if (y * kPage >= valid) continue;
-        float *dst = scores + ((kPair * (warp + k * kWarps) + y) * G + 2 * t) * kPage + ra;
-        if (2 * t < G) *reinterpret_cast<float2 *>(dst) = make_float2(s[y][0], s[y][2]);
-        if (2 * t + 1 < G) *reinterpret_cast<float2 *>(dst + kPage) = make_float2(s[y][1], s[y][3]);
+        float *dst = scores + ((kPair * (warp + k * kWarps) + y) * G + head_of_lane) * kPage + ra;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (head_of_lane + c < G) *reinterpret_cast<float2 *>(dst + c * kPage) = make_float2(s[y][c], s[y][C + c]);
       }
     }
 
     // 2. lazy running maximum
-    float c0 = fmaxf(s[0][0], s[0][2]), c1 = fmaxf(s[0][1], s[0][3]);
+    float top[C];
+    bool above = false;
 #pragma unroll
-    for (int y = 1; y < kPair; ++y) {
-      c0 = fmaxf(c0, fmaxf(s[y][0], s[y][2]));
-      c1 = fmaxf(c1, fmaxf(s[y][1], s[y][3]));
+    for (int c = 0; c < C; ++c) {
+      top[c] = fmaxf(fmaxf(s[0][c], s[0][C + c]), fmaxf(s[1][c], s[1][C + c]));
+      above |= top[c] > m[c] + kLazy;
     }
-    if (__any_sync(0xffffffffu, c0 > m0 + kLazy || c1 > m1 + kLazy)) {
-      float n0 = fmaxf(c0, m0), n1 = fmaxf(c1, m1);
+    if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
-        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-      }
-      const float a0 = attn_ex2(m0 - n0), a1 = attn_ex2(m1 - n1);  // n0, n1 > -inf: a slot has a row
-      m0 = n0;
-      m1 = n1;
+      for (int c = 0; c < C; ++c) {
+        float now = fmaxf(top[c], m[c]);
 #pragma unroll
-      for (int i = 0; i < S::kTiles; ++i) {
-        o[i][0] *= a0;
-        o[i][1] *= a1;
-        o[i][2] *= a0;
-        o[i][3] *= a1;
+        for (int x = 4; x < 32; x <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+        const float f = attn_ex2(m[c] - now);  // now > -inf: a slot has a row
+        m[c] = now;
+#pragma unroll
+        for (int i = 0; i < S::kTiles; ++i) {
+          o[i][c] *= f;
+          o[i][C + c] *= f;
+        }
+        e[c] *= f;
+        e[C + c] *= f;
       }
-      e[0] *= a0;
-      e[1] *= a1;
-      e[2] *= a0;
-      e[3] *= a1;
     }
-    // 3. P as three bf16 terms, transposed into the second product's fragments
+    // 3. P as three bf16 terms, transposed into the second product's fragments.
+    // The pairs that are rounded together are the two rows (C = 1) or the two heads.
     uint32_t bp[kPair][kPt][2];
 #pragma unroll
-    for (int y = 0; y < kPair; ++y)
+    for (int y = 0; y < kPair; ++y) {
+      uint32_t h[C], l[C], r[C];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float p0 = attn_ex2(s[y][2 * x] - m0), p1 = attn_ex2(s[y][2 * x + 1] - m1);
-        const uint32_t h = pack_bf16(p0, p1);
-        const float r0 = p0 - bf16_lo(h), r1 = p1 - bf16_hi(h);
-        const uint32_t l = pack_bf16(r0, r1);
-        const uint32_t r = pack_bf16(r0 - bf16_lo(l), r1 - bf16_hi(l));
-        if constexpr (GP == 4) {
-          bp[y][0][x] = transpose8x8(t < 2 ? h : l);
-          bp[y][1][x] = transpose8x8(t < 2 ? r : 0u);
-        } else {
-          bp[y][0][x] = transpose8x8(h);
-          bp[y][1][x] = transpose8x8(l);
-          bp[y][kPt - 1][x] = transpose8x8(r);
+      for (int i = 0; i < C; ++i) {
+        const int at = C == 1 ? 0 : C * i;  // of s: the pair is at and at + 1
+        const float p0 = attn_ex2(s[y][at] - m[0]), p1 = attn_ex2(s[y][at + 1] - m[C - 1]);
+        h[i] = pack_bf16(p0, p1);
+        const float r0 = p0 - bf16_lo(h[i]), r1 = p1 - bf16_hi(h[i]);
+        l[i] = pack_bf16(r0, r1);
+        // what is left has eight bits
+        r[i] = __byte_perm(__float_as_uint(r0 - bf16_lo(l[i])), __float_as_uint(r1 - bf16_hi(l[i])), 0x7632);
+      }
+      if constexpr (C == 1) {  // columns 2t and 2t + 1: the first two terms; the third and nothing
+        bp[y][0][0] = transpose8x8(__byte_perm(h[0], l[0], 0x5410));
+        bp[y][0][1] = transpose8x8(__byte_perm(h[0], l[0], 0x7632));
+        bp[y][1][0] = transpose8x8(r[0] & 0xffffu);
+        bp[y][1][1] = transpose8x8(r[0] >> 16);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          bp[y][0][x] = transpose8x8(h[x % C]);
+          bp[y][1][x] = transpose8x8(l[x % C]);
+          bp[y][kPt - 1][x] = transpose8x8(r[x % C]);
         }
       }
+    }
     // 4. O^T += V^T . P^T.  Each tile's products of the slot are a chain of their
     // own, added to the running sum in fp32: the tensor cores truncate what they
     // add to, which over a long chain would leave 1e-6 of the result.
@@ -538,8 +555,7 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
             mma16816(te, ma, kOnes, mb, kOnes, bp[y][x][0], bp[y][x][1]);
         }
       }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) e[x] += te[x];
+      add_tile(e, te);
     }
     // codes: D = 128: lane n's channels 16n + i (word 0: rows n of tile i) and 16n + 8 + i (word 1: rows n + 8);
     // D = 64: channels 8n + i and 8n + 4 + i, the halves of one word
@@ -582,11 +598,8 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
           }
         }
       }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        o[2 * j][x] += t0[x];
-        o[2 * j + 1][x] += t1[x];
-      }
+      add_tile(o[2 * j], t0);
+      add_tile(o[2 * j + 1], t1);
     }
     __syncwarp();  // every lane has read the slot
     if (k + kStages < n_my) issue_pair(k + kStages);
@@ -603,30 +616,21 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
     return;
   }
 
-  // the low terms of P sit two lanes on (GP = 4)
-#pragma unroll
-  for (int i = 0; i < S::kTiles; ++i)
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if constexpr (GP == 4) o[i][x] += __shfl_xor_sync(0xffffffffu, o[i][x], 2);
-  if constexpr (GP == 4)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) e[x] += __shfl_xor_sync(0xffffffffu, e[x], 2);
   __syncthreads();  // every warp is past its loop: the page slots are free
   float *red = reinterpret_cast<float *>(smem);  // [kWarps][G][D]
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int g = 2 * t + x;
-    if (g >= G || (GP == 4 && t >= 2)) continue;
+  for (int c = 0; c < C; ++c) {
+    const int g = head_of_lane + c;
+    if (g >= G) continue;
     float *dst = red + (warp * G + g) * D + n * (D / 8);
 #pragma unroll
     for (int i = 0; i < S::kTiles; ++i) {
-      dst[i] = fmaf(o[i][x], 0x1p64f, e[x]);
-      dst[S::kTiles + i] = fmaf(o[i][2 + x], 0x1p64f, e[x]);
+      dst[i] = fmaf(o[i][c], 0x1p64f, e[c]);
+      dst[S::kTiles + i] = fmaf(o[i][C + c], 0x1p64f, e[c]);
     }
     if (n == 0) {
-      m_s[warp * G + g] = x ? m1 : m0;
-      l_s[warp * G + g] = e[2 + x];
+      m_s[warp * G + g] = m[c];
+      l_s[warp * G + g] = e[C + c];
     }
   }
   __syncthreads();
