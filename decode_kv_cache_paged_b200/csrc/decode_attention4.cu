@@ -702,18 +702,17 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
 // The step without weights.
 //   * With units enough to give every warp slot of the GPU one and a half, a
 //     unit is one warp's: no merge, and the start and end of a unit cost a
-//     quarter of what four warps pay (2048 rows, 4096 units: 296 us against
-//     322; 1024 units: 105 against 91).
+//     quarter of what four warps pay (2048 rows, 4096 units: 272 us against
+//     290; 1024 units: 109 against 83).
 //   * A few long requests are split without a cluster: the SMs take at most
 //     seven clusters of 16 with a CTA each, so that clusters share SMs while
-//     others idle (8 units of 32768 rows: 26 us against 36).
+//     others idle (8 units of 32768 rows: 23 us against 35).
 //   * So are units whose CTAs do not all fit at once: a cluster waits until
 //     places for all its CTAs are free together, and gives none back before its
-//     last CTA is done (512 units of 4096 to 32768 rows, 8 heads: 452 us against
-//     555, 4 heads: 372 against 409; 64 units of 16384 rows, 4 heads: 58 against
-//     72).  The merge launch costs more than that where they do fit (64 units of
-//     4096 rows: 25 against 23) or are only pairs (512 units of 4096 rows: 98
-//     against 95).
+//     last CTA is done (512 units of 4096 to 32768 rows, 8 heads: 454 us against
+//     539, 4 heads: 338 against 373).  The merge launch costs more than that where
+//     they do fit (64 units of 8192 rows: 36 against 33) or are only pairs (512
+//     units of 8192 rows: 160 against 155).
 //   The partials of a split must fit the workspace (p.max_splits), and no fewer
 //   than half the CTAs that the rule asks for will do.
 template <int D, int GP>
@@ -729,19 +728,21 @@ cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, 
 }
 
 // With weights the scores stay in shared memory unless a CTA of the largest
-// cluster would have to keep more than 36 KB of them, or 20 KB where units
-// abound (18432 and 10240 rows at 8 heads): then too few warps fit an SM, and
-// the weights take a launch of their own that reads the keys again.  Us in one
-// launch and in two: 8 heads, 512 units of 12288 rows 507, 430, of 8192 rows
-// 311, 302, of 4096 to 32768 rows 1019, 644; 8 units of 32768 rows 62, 44, of
-// 12288 rows 23, 25.  4 heads, 512 units of 24576 rows 794, 697, of 16384 rows
-// 494, 474; 32 ragged units up to 32768 rows 50, 63; 2 heads, 512 units of 32768
-// rows 851, 902.
+// cluster would have to keep more than 36 KB of them, 20 KB from 128 units on or
+// 11 KB from 384 units on (at 8 heads 18432, 10240 and 5632 rows): then too few
+// warps fit an SM, and the weights take a launch of their own that reads the
+// keys again.  Us in one launch and in two: 512 units, 8 heads, of 4096 to 32768
+// rows 979, 645, of 12288 rows 510, 430, of 8192 rows 324, 303; 4 heads, of 24576
+// rows 770, 636, of 12288 rows 376, 335, of 8192 rows 216, 231; 2 heads, of 4096 to
+// 32768 rows 504, 497.  128 units, 4 heads, of 24576 rows 216, 181, of 16384 rows
+// 130, 138.  32 units of 32768 rows, 8 heads 124, 96, 4 heads 68, 74; 8 units 43,
+// 44 and 38, 40.
 template <int D, int GP>
 cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
   if (!p.weights) return launch4_step<D, GP>(p, G, np_max, sms, s);
   const size_t keep = (size_t)kPage * G * 4 * ((np_max + 15) / 16);
-  const size_t most = (int64_t)p.layer_count * p.R * p.hkv >= 128 ? 20 * 1024 : 36 * 1024;
+  const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
+  const size_t most = (units >= 384 ? 11 : units >= 128 ? 20 : 36) * 1024;
   if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
