@@ -680,8 +680,9 @@ template <int D, int GP, Mode4 MODE, int W, int ST>
 cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
   auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
   p.part_o = p.part_ml = nullptr;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kFit4<GP, MODE, W>, kRing4<D, MODE, W, ST>,
-                             MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W, MODE != kWeights, s);
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kFit4<GP, MODE, W>,
+                             kRing4<D, MODE, W, ST>, MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W,
+                             MODE != kWeights, s);
 }
 
 // A unit split over `splits` CTAs that are no cluster, and a launch that merges them.
@@ -723,7 +724,8 @@ cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, 
   if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
   const int cs = cluster_size(units, np_max, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4, 2>, 0);
   const int parts = std::min(cs, p.max_splits);
-  if (parts >= 4 && 2 * parts > cs && units * parts > (int64_t)kFit4<GP, kStep, 4> * sms) return launch4_split<D, GP, 4>(p, G, parts, s);
+  if (parts >= 4 && 2 * parts > cs && units * parts > (int64_t)kFit4<GP, kStep, 4> * sms)
+    return launch4_split<D, GP, 4>(p, G, parts, s);
   return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
 }
 
@@ -761,9 +763,10 @@ cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, 
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e;
   // the same limit for every launch: two threads' calls may interleave
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem)) != cudaSuccess) return e;
-  if (cs > 8 && cluster && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-    return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  if (e == cudaSuccess && cs > 8 && cluster)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   p.nsplit = cs;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * cs));

@@ -2,8 +2,8 @@
 
 Tolerance of the attention (u = 2^-24).  The scores' products of codes and the integer parts of the query are exact, and
 so are their sums (integers below 2^21); the rest of the query is at most 1/2 beside integers up to 2047 and its 16-term
-products may lose 2u of their largest each.  s and lo join them in fp32: 12 roundings per score, scaling, the subtraction of
-the maximum and exp2 add four.  With A = max_j scale*(sum_i |q_i| step code_ji + sum_g |lo_jg| sum_{i in g} |q_i|):
+products may lose 2u of their largest each (with 8 heads they are added to the integers' sums and may lose 2u of those).
+s and lo join them in fp32: 12 roundings per score, scaling, the subtraction of the maximum and exp2 add four.  With A = max_j scale*(sum_i |q_i| step code_ji + sum_g |lo_jg| sum_{i in g} |q_i|):
   score error  ds <= 16 u A + 2u*|s - m| + 4u; 4 (d/16 + 5) u A is used, which is above it.
 A weight enters the second product as three bf16 numbers that hold all of its bits; the tensor cores may truncate 2u of the
 largest of 16 products each, in a chain of at most 6, and the running sums take L/32 additions, the merges 64 more:
