@@ -69,7 +69,7 @@ struct AttnMerge {
   float part[W][8];                    // the warps' factors
   float all_m[16][8], all_l[16][8];    // every CTA's
   float fac[16][8];                    // exp2(m of the CTA - m of the unit) / sum of the unit
-  float lse2[8];                       // the unit's log2-sum-exp2
+  float lse2[8];                       // the unit's log2-sum-exp2 (+inf: reads as without rows)
 };
 
 // Adds the weights of this CTA's rows from their base-2 scores [page][G][16].
@@ -132,13 +132,20 @@ __device__ __forceinline__ void attn_write_lse(const DecodeAttnParams &p, int64_
 //   red:  [W][G][D] the warps' sums, m_s, l_s: [W][G] their maxima and sums
 //         (a warp without rows has l = 0); the caller has synchronised.
 //   scores: [pages of this CTA][G][16] base-2 scores, or null (no weights).
+// A head whose sum is 0 or, unless KEEP_NAN (the 4-bit cache), NaN reads as one
+// without rows: out = 0, lse = -inf, no weights.
 // Every thread of the CTA calls it.
-template <int D, int W, int NT>
+template <int D, int W, int NT, bool KEEP_NAN>
 __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const AttnUnit &u, int G, float *red,
-                                            const float *m_s, const float *l_s, AttnMerge<W> &mg, const float *scores) {
+                                            const float *m_s, const float *l_s, AttnMerge<W> &mg, float *scores) {
   const int tid = threadIdx.x;
   const int64_t head0 = ((int64_t)u.lc * p.R + u.r) * p.hq + (int64_t)u.h * G;
   const bool alone = u.cs == 1 && !p.part_o;
+  auto finish_head = [&](int g, float M, float L, bool none, bool write) {
+    const float lse2 = M + log2f(L);
+    mg.lse2[g] = none ? INFINITY : lse2;
+    if (write) attn_write_lse(p, head0 + g, u.len > 0 && !none ? lse2 : -INFINITY);
+  };
   // the warps' factors; a CTA that has the unit to itself divides by the sum at once
   for (int i = tid; i < W * 8; i += NT) {
     const int w = i >> 3, g = i & 7;
@@ -150,7 +157,8 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
     for (int x = 0; x < W; ++x)
       if (l_s[x * G + g] != 0.f) L = fmaf(l_s[x * G + g], attn_ex2(m_s[x * G + g] - M), L);
     const float f = l_s[w * G + g] != 0.f ? attn_ex2(m_s[w * G + g] - M) : 0.f;
-    mg.part[w][g] = !alone || f == 0.f ? f : f / L;
+    const bool none = !KEEP_NAN && !(L > 0.f);
+    mg.part[w][g] = !alone || f == 0.f ? f : none ? 0.f : f / L;
     if (w == 0) {
       mg.m[g] = M;
       mg.l[g] = L;
@@ -159,11 +167,7 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
         p.part_ml[pu * 2] = M;
         p.part_ml[pu * 2 + 1] = L;
       }
-      if (alone) {
-        const float lse2 = M + log2f(L);
-        mg.lse2[g] = lse2;
-        attn_write_lse(p, head0 + g, u.len > 0 ? lse2 : -INFINITY);
-      }
+      if (alone) finish_head(g, M, L, none, true);
     }
   }
   __syncthreads();
@@ -199,12 +203,9 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
       for (int x = 0; x < u.cs; ++x) M = fmaxf(M, mg.all_m[x][g]);
       for (int x = 0; x < u.cs; ++x)
         if (mg.all_l[x][g] != 0.f) L = fmaf(mg.all_l[x][g], attn_ex2(mg.all_m[x][g] - M), L);
-      mg.fac[c][g] = mg.all_l[c][g] != 0.f ? attn_ex2(mg.all_m[c][g] - M) / L : 0.f;
-      if (c == 0) {
-        const float lse2 = M + log2f(L);
-        mg.lse2[g] = lse2;
-        if (u.rank == 0) attn_write_lse(p, head0 + g, u.len > 0 ? lse2 : -INFINITY);
-      }
+      const bool none = !KEEP_NAN && !(L > 0.f);
+      mg.fac[c][g] = mg.all_l[c][g] != 0.f && !none ? attn_ex2(mg.all_m[c][g] - M) / L : 0.f;
+      if (c == 0) finish_head(g, M, L, none, u.rank == 0);
     }
     __syncthreads();
     // outputs: each CTA of the cluster writes its share of the G * D values
@@ -223,6 +224,16 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
     float lse2[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) lse2[x] = x < G ? mg.lse2[x] : 0.f;
+    if constexpr (!KEEP_NAN) {  // heads that read as ones without rows: no score of theirs counts
+      float top = lse2[0];
+#pragma unroll
+      for (int x = 1; x < 8; ++x) top = fmaxf(top, lse2[x]);
+      if (top == INFINITY) {
+        for (int i = tid; i < (u.pg1 - u.pg0) * kPage * G; i += NT)
+          if (mg.lse2[i / kPage % G] == INFINITY) scores[i] = -INFINITY;
+        __syncthreads();
+      }
+    }
     switch (G) {
       case 1: attn_add_weights<NT, 1>(p, u, lse2, scores); break;
       case 2: attn_add_weights<NT, 2>(p, u, lse2, scores); break;

@@ -7,7 +7,9 @@
 // read): s_j = scale * q . k_j, out = sum_j softmax(s)_j v_j and
 // lse = log sum_j exp(s_j), with query head hq reading KV head hq / G.  The
 // rows of a segment may sit in any slot order (hole-filling compaction):
-// attention does not depend on it.
+// attention does not depend on it.  A score of -infinity has weight 0; a head
+// with a NaN or +infinite score, or with none above -infinity, reads as one
+// without rows (out = 0, lse = -inf, no weights) however its rows are split.
 //
 // Design (B200): the kernel is HBM-bound (each K and V byte is used by the
 // G query heads of its KV head only, 2G flop per element), so it runs on the
@@ -40,6 +42,8 @@
 // kDevTimeout in the status word, lets its own copies land (bounded) and
 // leaves, all threads of the CTA together.
 #include <cuda_bf16.h>
+
+#include <cfloat>
 
 #include "attn_cluster.cuh"
 
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   float2 acc[G][S::kAccPairs];
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
-    m_run[k] = -INFINITY;
+    m_run[k] = -FLT_MAX;  // never -inf: rows of that score have weight exp2(-inf) = 0, not exp2(-inf + inf)
     l_lane[k] = 0.f;
   }
 #pragma unroll
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
       for (int b = 1; b < S::kBatches; ++b) mx = fmaxf(mx, sv[b][kk]);
 #pragma unroll
       for (int m = S::kHeadMask; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-      const float m_new = fmaxf(m_run[kk], mx);  // finite: a page has a valid row
+      const float m_new = fmaxf(m_run[kk], mx);
       alpha[kk] = exp2f(m_run[kk] - m_new);
       m_run[kk] = m_new;
       float ps = 0.f;
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
   __syncthreads();
   if constexpr (ACC) {
     __shared__ AttnMerge<W> mg;
-    attn_finish<D, W, kThreads>(p, un, G, red, &m_s[0][0], &l_s[0][0], mg, scores);
+    attn_finish<D, W, kThreads, false>(p, un, G, red, &m_s[0][0], &l_s[0][0], mg, scores);
     return;
   }
   const int64_t head0 = ((int64_t)lc * p.R + r) * p.hq + (int64_t)h * G;  // first query head row
@@ -456,14 +460,12 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
 #pragma unroll
     for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w][g]);
     float o = 0.f, lsum = 0.f;
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (m_s[w][g] == -INFINITY) continue;
-        const float sc = exp2f(m_s[w][g] - M);
-        o = fmaf(red[(w * G + g) * D + (i % D)], sc, o);
-        lsum = fmaf(l_s[w][g], sc, lsum);
-      }
+    for (int w = 0; w < W; ++w) {
+      if (l_s[w][g] == 0.f) continue;  // no rows, or none with a weight; a NaN stays one
+      const float sc = exp2f(m_s[w][g] - M);
+      o = fmaf(red[(w * G + g) * D + (i % D)], sc, o);
+      lsum = fmaf(l_s[w][g], sc, lsum);
     }
     if (p.nsplit == 1) {
       p.out[head0 * D + i] = lsum > 0.f ? o / lsum : 0.f;
@@ -484,7 +486,8 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
 // waits for memory twice and not once per split (one bf16 request of 32768 rows,
 // 8 KV heads, 16 splits: 48 us for the step, 69 with a loop per output).
 // A sum that is NaN counts as no rows, as in a step without splits, unless
-// keep_nan (the 4-bit cache, whose broken groups show as NaN).
+// keep_nan (the 4-bit cache, whose broken groups show as NaN): attn_finish has
+// the same rule.
 __global__ void decode_attention_merge_kernel(DecodeAttnParams p, int D, bool keep_nan) {
   const int64_t head = blockIdx.x, pu0 = head * p.nsplit;
   const int c = threadIdx.x;

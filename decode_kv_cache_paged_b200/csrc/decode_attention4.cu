@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
     }
   }
   __syncthreads();
-  attn_finish<D, kWarps, kThreads>(p, u, G, red, m_s, l_s, mg, MODE == kStepWeights ? scores : nullptr);
+  attn_finish<D, kWarps, kThreads, true>(p, u, G, red, m_s, l_s, mg, MODE == kStepWeights ? scores : nullptr);
 }
 
 // Cluster size: CTAs that share a unit, a power of two up to 16, so that every
