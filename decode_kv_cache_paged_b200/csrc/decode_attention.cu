@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(kThreads) decode_attention_kernel(DecodeAttnPa
     un.lc = unit / (p.nsplit * p.hkv * p.R);
     un.l = p.layer_begin + un.lc;
     un.len = p.lengths[un.r];
-    un.pg0 = un.rank * p.pages_per_split;
-    un.pg1 = min((un.len + kPage - 1) / kPage, un.pg0 + p.pages_per_split);
+    const int n_pages = (un.len + kPage - 1) / kPage;
+    const int per = p.pages_per_split ? p.pages_per_split : attn_pages_per_split(n_pages, p.nsplit);
+    un.pg0 = un.rank * per;
+    un.pg1 = min(n_pages, un.pg0 + per);
   }
   const int split = un.rank, h = un.h, r = un.r, lc = un.lc, l = un.l, len = un.len, pg0 = un.pg0, pg1 = un.pg1;
   const int n_my = pg1 - pg0 > warp ? (pg1 - pg0 - warp + W - 1) / W : 0;  // pages of this warp

@@ -916,18 +916,17 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   // a captured step may be replayed over a longer cache than today's
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
-  const int np_max = cap == cudaStreamCaptureStatusNone ? (max_len + kPage - 1) / kPage : ctx->maxp;
-  // splits: enough CTAs for two waves of two CTAs per SM, pages of a split a
-  // multiple of the 4-page tile, at least two tiles per split
+  const bool captured = cap != cudaStreamCaptureStatusNone;
+  const int np_max = captured ? (int)std::min<int64_t>(ctx->maxp, c.num_pages) : (max_len + kPage - 1) / kPage;
+  // splits: enough CTAs for two waves of two CTAs per SM.  A captured step has
+  // splits for the longest rows and takes each request's share of them on the
+  // device (pages_per_split 0): one that was fixed here for 32768 rows left a
+  // request of 2048 to one split (8 KV heads, 4 query heads each, bf16: 41 us, now 8).
   const int64_t base = (int64_t)layer_count * R * c.num_kv_heads;
-  int nsplit = 1;
-  if (np_max > 0) {
-    const int64_t want = (4LL * ctx->num_sms + base - 1) / base;
-    nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({want, kAttnSplits / layer_count, (np_max + 7) / 8}));
-  }
-  int pps = std::max(1, (np_max + nsplit - 1) / nsplit);
-  pps = (pps + 3) & ~3;
-  nsplit = std::max(1, (np_max + pps - 1) / pps);
+  const int64_t want = (4LL * ctx->num_sms + base - 1) / base;
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(want, kAttnSplits / layer_count));
+  const int pps = captured ? 0 : attn_pages_per_split(np_max, most);
+  const int nsplit = captured ? std::max(1, std::min(most, (np_max + 7) / 8)) : std::max(1, (np_max + pps - 1) / pps);
   DecodeAttnParams p{};
   p.k_pool = ctx->k_pool;
   p.v_pool = ctx->v_pool;

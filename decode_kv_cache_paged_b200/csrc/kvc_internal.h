@@ -66,7 +66,9 @@ struct DecodeAttnParams {
   int32_t *status;
   int64_t num_pages;
   int32_t bt_stride, layer_begin, layer_count, R, hkv, hq;
-  int32_t nsplit, pages_per_split;  // CTAs of a unit (cluster forms: of its cluster); pages of each (not used there)
+  // CTAs of a unit (cluster forms: of its cluster); pages of each, 0 = from each
+  // request's length, in at most nsplit splits (not used in the cluster forms)
+  int32_t nsplit, pages_per_split;
   float qscale;                // scale * log2(e)
   float *weights;              // accumulated attention weights, indexed like the position map, or null
   float decay;                 // weights <- decay * weights + this step's
@@ -106,6 +108,13 @@ struct BeaconScoreParams {
   int64_t total_segs;         // R * layers * Hkv (rows of the beacon arrays / B)
   int32_t bt_stride, layers, hkv, B, d, dtype, max_seq;
 };
+
+// Pages of a split of n_pages pages in at most `most` splits: a multiple of the
+// 4-page tile, and at least two tiles a split.
+__host__ __device__ inline int attn_pages_per_split(int n_pages, int most) {
+  const int tiles2 = (n_pages + 7) / 8, n = most < tiles2 ? most : tiles2 > 1 ? tiles2 : 1;
+  return n_pages > 0 ? ((n_pages + n - 1) / n + 3) & ~3 : 4;
+}
 
 // Kernel launchers (each returns the launch error, if any).
 cudaError_t launch_bt_scatter(const int32_t *pairs, int n, int32_t *block_table, cudaStream_t s);
