@@ -531,20 +531,20 @@ cudaError_t launch_typed(const DecodeAttnParams &p, int units, cudaStream_t s) {
 }
 
 template <typename T, int D, int G>
-cudaError_t launch_acc(DecodeAttnParams p, int np_max, int sms, cudaStream_t s) {
+cudaError_t launch_acc(DecodeAttnParams p, AttnPages np, int sms, cudaStream_t s) {
   auto kernel = decode_attention_kernel<T, D, G, true>;
   p.part_o = p.part_ml = nullptr;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, 3, AttnShape<T, D, G>::kSmem,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np, sms, 3, AttnShape<T, D, G>::kSmem,
                              (size_t)kPage * G * 4, kThreads, true, s);
 }
 
 template <typename T, int D>
-cudaError_t launch_acc_g(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
+cudaError_t launch_acc_g(const DecodeAttnParams &p, int G, AttnPages np, int sms, cudaStream_t s) {
   switch (G) {
-    case 1: return launch_acc<T, D, 1>(p, np_max, sms, s);
-    case 2: return launch_acc<T, D, 2>(p, np_max, sms, s);
-    case 4: return launch_acc<T, D, 4>(p, np_max, sms, s);
-    default: return launch_acc<T, D, 8>(p, np_max, sms, s);
+    case 1: return launch_acc<T, D, 1>(p, np, sms, s);
+    case 2: return launch_acc<T, D, 2>(p, np, sms, s);
+    case 4: return launch_acc<T, D, 4>(p, np, sms, s);
+    default: return launch_acc<T, D, 8>(p, np, sms, s);
   }
 }
 
@@ -565,12 +565,12 @@ bool decode_attention_supported(int dtype, int head_dim, int G) {
          (G == 1 || G == 2 || G == 4 || G == 8);
 }
 
-cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, int np_max, int sms,
+cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, AttnPages np, int sms,
                                         cudaStream_t s) {
   if (dtype == KVC_BF16)
-    return head_dim == 128 ? launch_acc_g<__nv_bfloat16, 128>(p, G, np_max, sms, s)
-                           : launch_acc_g<__nv_bfloat16, 64>(p, G, np_max, sms, s);
-  return head_dim == 128 ? launch_acc_g<float, 128>(p, G, np_max, sms, s) : launch_acc_g<float, 64>(p, G, np_max, sms, s);
+    return head_dim == 128 ? launch_acc_g<__nv_bfloat16, 128>(p, G, np, sms, s)
+                           : launch_acc_g<__nv_bfloat16, 64>(p, G, np, sms, s);
+  return head_dim == 128 ? launch_acc_g<float, 128>(p, G, np, sms, s) : launch_acc_g<float, 64>(p, G, np, sms, s);
 }
 
 cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, bool keep_nan, cudaStream_t s) {

@@ -652,35 +652,65 @@ __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_
 // 61, *49, 62; without weights, 4 heads, 64 units of 8192 rows 91, 52, *36, 33; 512
 // units of 2048 rows *54, 62, 66; bf16 with weights, 32 units of 16384 rows -, 154,
 // 82, *58, 83 (* the rule's).
-int cluster_size(int64_t units, int np_max, int sms, int warps, int fit, size_t base_smem, size_t page_smem) {
-  constexpr double kFixed = 48;
-  constexpr size_t kSm = 228 * 1024, kCta = 1024 + 2304;  // shared memory of an SM; a CTA's beside the dynamic
-  int best = 16;
-  double least = 1e300;
-  for (int cs = 1; cs <= 16; cs *= 2) {
-    if (cs > 1 && (np_max + cs / 2 - 1) / (cs / 2) <= 2 * warps) break;
-    const int share = (np_max + cs - 1) / cs;
-    const size_t smem = base_smem + page_smem * share;
-    if (smem > kMaxSmem || (share > 256 && cs < 16)) continue;
-    const int slots = std::max(1, std::min(fit, (int)(kSm / (smem + kCta))));
+// A captured launch (np.now below np.most) runs over any length up to np.most, with
+// shared memory for that: of the sizes that fit, the one with the least product of
+// the estimated times over today's rows and over the longest (so neither is much
+// above its best).  Us of a step over 2048 rows in a context of 32768 planned for
+// the longest rows alone, so, and called: 4 bits, 512 units 67, 48, 51; 8 heads, 512
+// units of up to 2048 rows 84, 51, 47; with weights, 2048 units 369, 224, 189; bf16
+// with weights, 1024 units 681, 458, 187, 64 units 44, 29, 21.  The price, over 30000
+// rows: 4 bits, 512 units 515, 586, 517; bf16 with weights, 64 units 242, 279, 242.
+struct ClusterRule {
+  int64_t units;
+  int sms, warps, fit;
+  size_t base_smem, page_smem;
+
+  size_t smem(int cs, int pages) const { return base_smem + page_smem * ((pages + cs - 1) / cs); }
+  // estimated time over `pages` pages a unit with shared memory for `most`
+  double cost(int cs, int pages, int most) const {
+    constexpr double kFixed = 48;
+    constexpr size_t kSm = 228 * 1024, kCta = 1024 + 2304;  // shared memory of an SM; a CTA's beside the dynamic
+    const int share = (pages + cs - 1) / cs;
+    const int slots = std::max(1, std::min(fit, (int)(kSm / (smem(cs, most) + kCta))));
     const double ctas = (double)units * cs, waves = ctas / ((double)sms * slots);
     const int a = std::min<int64_t>(slots, (units * cs + sms - 1) / sms);
-    const double cost = (waves <= 1 ? 1 : 0.25 * waves + 0.75 * std::ceil(waves)) * (share + kFixed) * a /
-                        (1 - std::exp2(-a * warps / 4.0));
-    if (cost < least) least = cost, best = cs;
+    return (waves <= 1 ? 1 : 0.25 * waves + 0.75 * std::ceil(waves)) * (share + kFixed) * a /
+           (1 - std::exp2(-a * warps / 4.0));
   }
-  return best;
-}
+  // the size for launches over `pages` pages a unit
+  int best(int pages) const {
+    int at = 16;
+    double least = 1e300;
+    for (int cs = 1; cs <= 16 && !too_many(cs, pages); cs *= 2) {
+      if (smem(cs, pages) > kMaxSmem || ((pages + cs - 1) / cs > 256 && cs < 16)) continue;
+      if (const double c = cost(cs, pages, pages); c < least) least = c, at = cs;
+    }
+    return at;
+  }
+  bool too_many(int cs, int pages) const { return cs > 1 && (pages + cs / 2 - 1) / (cs / 2) <= 2 * warps; }
+  int operator()(AttnPages np) const {
+    const int most = best(np.most);
+    if (np.now >= np.most) return most;
+    int at = most;
+    double least = 1e300;
+    for (int cs = 1; cs <= 16 && !too_many(cs, np.most); cs *= 2) {
+      if (smem(cs, np.most) > kMaxSmem) continue;
+      const double c = cost(cs, np.now, np.most) * cost(cs, np.most, np.most);
+      if (c < least) least = c, at = cs;
+    }
+    return at;
+  }
+};
 
 // shared memory of the page slots
 template <int D, Mode4 MODE, int W, int ST>
 constexpr size_t kRing4 = 128 + (size_t)W * ST * kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
 
 template <int D, int GP, Mode4 MODE, int W, int ST>
-cudaError_t launch4_w(DecodeAttnParams p, int G, int np_max, int sms, cudaStream_t s) {
+cudaError_t launch4_w(DecodeAttnParams p, int G, AttnPages np, int sms, cudaStream_t s) {
   auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
   p.part_o = p.part_ml = nullptr;
-  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np_max, sms, kFit4<GP, MODE, W>,
+  return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np, sms, kFit4<GP, MODE, W>,
                              kRing4<D, MODE, W, ST>, MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W,
                              MODE != kWeights, s);
 }
@@ -704,7 +734,8 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
 //   * With units enough to give every warp slot of the GPU one and a half, a
 //     unit is one warp's: no merge, and the start and end of a unit cost a
 //     quarter of what four warps pay (2048 rows, 4096 units: 272 us against
-//     290; 1024 units: 109 against 83).
+//     290; 1024 units: 109 against 83).  A captured launch keeps the form over
+//     longer rows (4096 units of 8192 rows 1038 us, clusters 1069).
 //   * A few long requests are split without a cluster: the SMs take at most
 //     seven clusters of 16 with a CTA each, so that clusters share SMs while
 //     others idle (8 units of 32768 rows: 23 us against 35).
@@ -717,16 +748,17 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
 //   The partials of a split must fit the workspace (p.max_splits), and no fewer
 //   than half the CTAs that the rule asks for will do.
 template <int D, int GP>
-cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
+cudaError_t launch4_step(const DecodeAttnParams &p, int G, AttnPages np, int sms, cudaStream_t s) {
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
-  if (units * 2 >= 16LL * sms * 3 && np_max <= 512) return launch4_w<D, GP, kStep, 1, 2>(p, G, np_max, sms, s);
-  const int splits = std::min({p.max_splits, (np_max + 15) / 16, (int)(2LL * sms / units)});
-  if (splits > 8 && np_max >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
-  const int cs = cluster_size(units, np_max, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4, 2>, 0);
+  if (units * 2 >= 16LL * sms * 3 && np.now <= 512)
+    return launch4_w<D, GP, kStep, 1, 2>(p, G, AttnPages{np.now, np.now}, sms, s);
+  const int splits = std::min({p.max_splits, (np.most + 15) / 16, (int)(2LL * sms / units)});
+  if (splits > 8 && np.most >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
+  const int cs = ClusterRule{units, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4, 2>, 0}(np);
   const int parts = std::min(cs, p.max_splits);
   if (parts >= 4 && 2 * parts > cs && units * parts > (int64_t)kFit4<GP, kStep, 4> * sms)
     return launch4_split<D, GP, 4>(p, G, parts, s);
-  return launch4_w<D, GP, kStep, 4, 2>(p, G, np_max, sms, s);
+  return launch4_w<D, GP, kStep, 4, 2>(p, G, np, sms, s);
 }
 
 // With weights the scores stay in shared memory unless a CTA of the largest
@@ -740,26 +772,27 @@ cudaError_t launch4_step(const DecodeAttnParams &p, int G, int np_max, int sms, 
 // 130, 138.  32 units of 32768 rows, 8 heads 124, 96, 4 heads 68, 74; 8 units 43,
 // 44 and 38, 40.
 template <int D, int GP>
-cudaError_t launch4(const DecodeAttnParams &p, int G, int np_max, int sms, cudaStream_t s) {
-  if (!p.weights) return launch4_step<D, GP>(p, G, np_max, sms, s);
-  const size_t keep = (size_t)kPage * G * 4 * ((np_max + 15) / 16);
+cudaError_t launch4(const DecodeAttnParams &p, int G, AttnPages np, int sms, cudaStream_t s) {
+  if (!p.weights) return launch4_step<D, GP>(p, G, np, sms, s);
+  const size_t keep = (size_t)kPage * G * 4 * ((np.most + 15) / 16);
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   const size_t most = (units >= 384 ? 11 : units >= 128 ? 20 : 36) * 1024;
-  if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np_max, sms, s);
+  if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
-  if (cudaError_t e = launch4_step<D, GP>(step, G, np_max, sms, s)) return e;
-  return launch4_w<D, GP, kWeights, 4, 2>(p, G, np_max, sms, s);
+  if (cudaError_t e = launch4_step<D, GP>(step, G, np, sms, s)) return e;
+  return launch4_w<D, GP, kWeights, 4, 2>(p, G, np, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, int fit,
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, AttnPages np, int sms, int fit,
                                 size_t base_smem, size_t page_smem, int threads, bool cluster, cudaStream_t s) {
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (units <= 0) return cudaSuccess;
-  const int cs = cluster_size(units, np_max, sms, threads / 32, fit, base_smem, page_smem);
-  const size_t smem = base_smem + page_smem * ((np_max + cs - 1) / cs);
+  const ClusterRule rule{units, sms, threads / 32, fit, base_smem, page_smem};
+  const int cs = rule(np);
+  const size_t smem = rule.smem(cs, np.most);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e;
   // the same limit for every launch: two threads' calls may interleave
@@ -783,10 +816,10 @@ cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, 
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
+cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, AttnPages np, int sms,
                                      cudaStream_t s) {
-  if (head_dim == 128) return G <= 4 ? launch4<128, 4>(p, G, np_max, sms, s) : launch4<128, 8>(p, G, np_max, sms, s);
-  return G <= 4 ? launch4<64, 4>(p, G, np_max, sms, s) : launch4<64, 8>(p, G, np_max, sms, s);
+  if (head_dim == 128) return G <= 4 ? launch4<128, 4>(p, G, np, sms, s) : launch4<128, 8>(p, G, np, sms, s);
+  return G <= 4 ? launch4<64, 4>(p, G, np, sms, s) : launch4<64, 8>(p, G, np, sms, s);
 }
 
 }  // namespace kvc

@@ -917,7 +917,8 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
   const bool captured = cap != cudaStreamCaptureStatusNone;
-  const int np_max = captured ? (int)std::min<int64_t>(ctx->maxp, c.num_pages) : (max_len + kPage - 1) / kPage;
+  const int np_now = (max_len + kPage - 1) / kPage;
+  const int np_max = captured ? (int)std::min<int64_t>(ctx->maxp, c.num_pages) : np_now;
   // splits: enough CTAs for two waves of two CTAs per SM.  A captured step has
   // splits for the longest rows and takes each request's share of them on the
   // device (pages_per_split 0): one that was fixed here for 32768 rows left a
@@ -960,8 +961,9 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   if (c.dtype != KVC_INT4 && !o.accumulate) {
     e = launch_decode_attention(p, c.head_dim, c.dtype, G, &launches, ctx->stream);
   } else {
-    e = c.dtype == KVC_INT4 ? launch_decode_attention4(p, c.head_dim, G, np_max, ctx->num_sms, ctx->stream)
-                            : launch_decode_attention_acc(p, c.head_dim, c.dtype, G, np_max, ctx->num_sms, ctx->stream);
+    e = c.dtype == KVC_INT4 ? launch_decode_attention4(p, c.head_dim, G, {np_now, np_max}, ctx->num_sms, ctx->stream)
+                            : launch_decode_attention_acc(p, c.head_dim, c.dtype, G, {np_now, np_max}, ctx->num_sms,
+                                                          ctx->stream);
   }
   if (e != cudaSuccess) return cuda_fail(ctx, e, "decode_attention");
   if (ms_out) {

@@ -116,6 +116,12 @@ __host__ __device__ inline int attn_pages_per_split(int n_pages, int most) {
   return n_pages > 0 ? ((n_pages + n - 1) / n + 3) & ~3 : 4;
 }
 
+// Pages of the longest request: now, and at most when the launch runs (more than
+// now only in a captured launch).
+struct AttnPages {
+  int now, most;
+};
+
 // Kernel launchers (each returns the launch error, if any).
 cudaError_t launch_bt_scatter(const int32_t *pairs, int n, int32_t *block_table, cudaStream_t s);
 cudaError_t launch_append_kv(const uint8_t *k_src, const uint8_t *v_src, uint8_t *k_pool,
@@ -146,18 +152,17 @@ bool decode_attention_supported(int dtype, int head_dim, int G);
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s);
 // The cluster forms (attn_cluster.cuh): over the 4-bit cache, and accumulating
-// weights over the other caches.  np_max: most pages a request may have when
-// the launch runs; sms: the device's SMs.
+// weights over the other caches.  sms: the device's SMs.
 // launch_attn_cluster picks how many CTAs share a unit and launches `kernel`
 // with (DecodeAttnParams, int G): fit is how many CTAs an SM's registers hold,
 // base_smem the kernel's shared memory without the scores, page_smem the bytes
 // of scores per page (0 without weights), cluster whether the CTAs of a unit
 // are a cluster.
-cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, int np_max, int sms, int fit,
+cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, AttnPages np, int sms, int fit,
                                 size_t base_smem, size_t page_smem, int threads, bool cluster, cudaStream_t s);
-cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, int np_max, int sms,
+cudaError_t launch_decode_attention4(const DecodeAttnParams &p, int head_dim, int G, AttnPages np, int sms,
                                      cudaStream_t s);
-cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, int np_max, int sms,
+cudaError_t launch_decode_attention_acc(const DecodeAttnParams &p, int head_dim, int dtype, int G, AttnPages np, int sms,
                                         cudaStream_t s);
 cudaError_t launch_select_compact(const SelectCompactParams &p, int mode, int n_seg_req,
                                   int max_n, int max_m, cudaStream_t s);

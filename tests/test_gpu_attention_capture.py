@@ -39,13 +39,16 @@ def timed_us(ctx, q, accumulate, captured, steps=8, repeats=7):
     return best
 
 
-# cache, requests, layers, KV heads, query heads a KV head, rows, whether the step accumulates
-SERVED = [("bf16", 1, 1, 8, 4, 2048, False), ("f32", 1, 1, 2, 4, 2048, False), ("bf16", 4, 1, 2, 4, 4096, False)]
+# cache, requests, layers, KV heads, query heads a KV head, rows, whether the step accumulates, and how many times the call's
+# time it may take (with weights it keeps shared memory for the scores of the longest rows)
+SERVED = [("bf16", 1, 1, 8, 4, 2048, False, 1.5), ("f32", 1, 1, 2, 4, 2048, False, 1.5), ("bf16", 4, 1, 2, 4, 4096, False, 1.5),
+          ("int4", 128, 4, 8, 4, 2048, False, 1.5), ("int4", 64, 8, 8, 8, 2048, False, 1.5), ("int4", 64, 1, 8, 8, 2048, False, 1.5),
+          ("int4", 1, 1, 8, 4, 2048, False, 1.5), ("int4", 128, 2, 8, 4, 2048, True, 1.5), ("bf16", 128, 1, 8, 4, 2048, True, 3.0)]
 
 
-@pytest.mark.parametrize("cache,R,layers,H,G,n,accumulate", SERVED)
-def test_a_captured_step_costs_what_the_call_does(cache, R, layers, H, G, n, accumulate):
-    """Rows far below the context's maximum, which a replay may reach: 1.5 times the call's time, and 5 us, are allowed."""
+@pytest.mark.parametrize("cache,R,layers,H,G,n,accumulate,times", SERVED)
+def test_a_captured_step_costs_what_the_call_does(cache, R, layers, H, G, n, accumulate, times):
+    """Rows far below the context's maximum, which a replay may reach: a multiple of the call's time, and 5 us, are allowed."""
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         ctx = Context(ContextSpec(num_requests=R, num_layers=layers, num_kv_heads=H, head_dim=128, max_seq_len=32768,
@@ -59,7 +62,7 @@ def test_a_captured_step_costs_what_the_call_does(cache, R, layers, H, G, n, acc
         called = timed_us(ctx, q, accumulate, False)
         captured = timed_us(ctx, q, accumulate, True)
         print(f"called {called:.1f} us, captured {captured:.1f} us")
-        assert captured <= 1.5 * called + 5
+        assert captured <= times * called + 5
         ctx.sync()
     ctx.close()
 
