@@ -558,7 +558,32 @@ cudaError_t launch_g(const DecodeAttnParams &p, int G, int units, cudaStream_t s
   }
 }
 
+template <typename T, int D, int G>
+cudaError_t load_typed() {
+  cudaFuncAttributes a;
+  if (cudaError_t e = cudaFuncGetAttributes(&a, decode_attention_kernel<T, D, G, false>)) return e;
+  return cudaFuncGetAttributes(&a, decode_attention_kernel<T, D, G, true>);
+}
+
+template <typename T, int D>
+cudaError_t load_g(int G) {
+  switch (G) {
+    case 1: return load_typed<T, D, 1>();
+    case 2: return load_typed<T, D, 2>();
+    case 4: return load_typed<T, D, 4>();
+    default: return load_typed<T, D, 8>();
+  }
+}
+
 }  // namespace
+
+cudaError_t load_decode_attention(int dtype, int head_dim, int G) {
+  cudaFuncAttributes a;
+  if (cudaError_t e = cudaFuncGetAttributes(&a, decode_attention_merge_kernel)) return e;
+  if (dtype == KVC_INT4) return load_decode_attention4(head_dim, G);
+  if (dtype == KVC_BF16) return head_dim == 128 ? load_g<__nv_bfloat16, 128>(G) : load_g<__nv_bfloat16, 64>(G);
+  return head_dim == 128 ? load_g<float, 128>(G) : load_g<float, 64>(G);
+}
 
 bool decode_attention_supported(int dtype, int head_dim, int G) {
   return (dtype == KVC_BF16 || dtype == KVC_F32 || dtype == KVC_INT4) && (head_dim == 64 || head_dim == 128) &&

@@ -784,7 +784,25 @@ cudaError_t launch4(const DecodeAttnParams &p, int G, AttnPages np, int sms, cud
   return launch4_w<D, GP, kWeights, 4, 2>(p, G, np, sms, s);
 }
 
+// Loads every form that launch4 may choose.
+template <int D, int GP>
+cudaError_t load4() {
+  cudaFuncAttributes a;
+  for (const void *kernel : {reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 1, 2>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 4, 2>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 8, 2>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStepWeights, 4, 2>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kWeights, 4, 2>)})
+    if (cudaError_t e = cudaFuncGetAttributes(&a, kernel)) return e;
+  return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t load_decode_attention4(int head_dim, int G) {
+  if (head_dim == 128) return G <= 4 ? load4<128, 4>() : load4<128, 8>();
+  return G <= 4 ? load4<64, 4>() : load4<64, 8>();
+}
 
 cudaError_t launch_attn_cluster(const void *kernel, DecodeAttnParams &p, int G, AttnPages np, int sms, int fit,
                                 size_t base_smem, size_t page_smem, int threads, bool cluster, cudaStream_t s) {

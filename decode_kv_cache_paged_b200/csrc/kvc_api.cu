@@ -154,6 +154,7 @@ struct kvc_ctx {
   float *weights = nullptr;  // accumulated attention weights (caller's buffer), indexed like d_pos
   int recent = 0;            // newest positions the attention selector always keeps
   float *d_attn = nullptr;
+  bool attn_loaded = false;  // the attention kernels of this type
   std::string err;
 };
 
@@ -917,6 +918,10 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(ctx->stream, &cap) != cudaSuccess) cudaGetLastError();
   const bool captured = cap != cudaStreamCaptureStatusNone;
+  if (!captured && !ctx->attn_loaded) {
+    if (cudaError_t e = load_decode_attention(c.dtype, c.head_dim, G)) return cuda_fail(ctx, e, "load_decode_attention");
+    ctx->attn_loaded = true;
+  }
   const int np_now = (max_len + kPage - 1) / kPage;
   const int np_max = captured ? (int)std::min<int64_t>(ctx->maxp, c.num_pages) : np_now;
   // splits: enough CTAs for two waves of two CTAs per SM.  A captured step has

@@ -149,6 +149,10 @@ cudaError_t launch_gather_dense(const uint8_t *k_pool, const uint8_t *v_pool,
 cudaError_t launch_wait_timeout_probe(int32_t *status, uint32_t limit_ms, cudaStream_t s);
 cudaError_t launch_decode_attention_merge(const DecodeAttnParams &p, int head_dim, bool keep_nan, cudaStream_t s);
 bool decode_attention_supported(int dtype, int head_dim, int G);
+// Loads the kernels of every form that a step of these types may launch, for a
+// capture to meet none for the first time.
+cudaError_t load_decode_attention(int dtype, int head_dim, int G);
+cudaError_t load_decode_attention4(int head_dim, int G);
 cudaError_t launch_decode_attention(const DecodeAttnParams &p, int head_dim, int dtype, int G, int *launches,
                                     cudaStream_t s);
 // The cluster forms (attn_cluster.cuh): over the 4-bit cache, and accumulating

@@ -340,12 +340,13 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *     the device time of its kernels, and reports latched device errors.
  * Enqueued on the context's stream; uses the context's workspace for split
  * partials, so calls on one context must not overlap.  Without ms_out the call
- * may be captured into a CUDA graph (after one call outside a capture, which
- * loads the kernels); a replay reads the cache as it stands then, rows appended
- * and rounds made since the capture included.  A captured step is planned for
- * requests of any length up to max_seq_len (and of today's); one that
- * accumulates weights keeps room for the scores of that many rows, so it is the
- * faster the closer max_seq_len is to the rows a request really reaches.
+ * may be captured into a CUDA graph, after one call on the context outside a
+ * capture, with any options, which loads all that a step may launch; a replay
+ * reads the cache as it stands then, rows appended and rounds made since the
+ * capture included.  A captured step is planned for requests of any length up
+ * to max_seq_len (and of today's); one that accumulates weights keeps room for
+ * the scores of that many rows, so it is the faster the closer max_seq_len is
+ * to the rows a request really reaches.
  * Errors (nothing enqueued): KVC_ERR_INVALID_ARG; KVC_ERR_UNSUPPORTED unless
  * head_dim is 64 or 128 and G in {1, 2, 4, 8}. */
 kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer_count, const void *q,

@@ -1,4 +1,10 @@
-"""Captured decode steps: planned for every length that a replay may meet, and as fast as the same step called."""
+"""Captured decode steps: planned for every length that a replay may meet, made of kernels that the call before the capture
+has loaded, and as fast as the same step called."""
+import json
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +14,8 @@ from test_gpu_attention_weights import CACHES, check_weights, dense_weights
 from test_gpu_int4 import check_attention, fill, make, rows
 
 pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 def timed_us(ctx, q, accumulate, captured, steps=8, repeats=7):
@@ -100,3 +108,96 @@ def test_replays_follow_the_lengths(first, then, cache, accumulate):
         side.synchronize()
         del graph
     ctx.close()
+
+
+# One short call, then a capture whose longest rows may be 32768, in a process that has loaded nothing before.  Prints the
+# kernels of the capture and those of them that the call had not loaded, and the largest difference from a call's outputs.
+FRESH = r"""
+import json, sys
+sys.path[:0] = {paths!r}
+import torch
+from cuda.bindings import driver as cu
+from decode_kv_cache_paged_b200 import Context, ContextSpec
+
+def ok(res):
+    assert res[0] == cu.CUresult.CUDA_SUCCESS, res
+    return res[1] if len(res) == 2 else res[1:]
+
+def functions(graph):
+    # the graph's kernel nodes
+    n = ok(cu.cuGraphGetNodes(graph, 0))[1]
+    for node in ok(cu.cuGraphGetNodes(graph, n))[0]:
+        if ok(cu.cuGraphNodeGetType(node)) == cu.CUgraphNodeType.CU_GRAPH_NODE_TYPE_KERNEL:
+            p = ok(cu.cuGraphKernelNodeGetParams(node))
+            yield p.func if int(p.func) else ok(cu.cuKernelGetFunction(p.kern))
+
+def name(f):
+    return ok(cu.cuFuncGetName(f)).decode()
+
+def capture(ctx, q, out, lse, acc):
+    s = side.cuda_stream
+    ok2 = cu.cuStreamBeginCapture(s, cu.CUstreamCaptureMode.CU_STREAM_CAPTURE_MODE_THREAD_LOCAL)
+    assert ok2[0] == cu.CUresult.CUDA_SUCCESS
+    ctx.decode_attention(q, out=out, lse=lse, accumulate=acc)
+    return ok(cu.cuStreamEndCapture(s))
+
+cache, d, G, R, longest, H, warm = {case!r}
+dtype = "int4" if cache == "int4" else getattr(torch, cache)
+side = torch.cuda.Stream()
+with torch.cuda.stream(side):
+    def context(max_len, dtype=dtype, d=d, G=G, R=R, H=H):
+        ctx = Context(ContextSpec(num_requests=R, num_layers=1, num_kv_heads=H, head_dim=d, max_seq_len=max_len,
+                                  num_pages=max(R * 8, max_len // 16), num_q_heads=H * G), dtype=dtype)
+        x = torch.randn((R, 1, 100, H, d), device="cuda").to(ctx.dtype)
+        ctx.append(list(range(R)), x, x)
+        return ctx
+    # the modules of the attention kernels: of a step over another cache, and of the call before the capture
+    modules = dict()
+    def step_of(ctx, acc):
+        q = torch.randn((1, ctx.spec.num_requests, ctx.num_q_heads, ctx.spec.head_dim), device="cuda").to(ctx.dtype)
+        out, lse = ctx.decode_attention(q, accumulate=acc)
+        side.synchronize()
+        for f in functions(capture(ctx, q, out, lse, acc)):
+            module = ok(cu.cuFuncGetModule(f))
+            modules[int(module)] = module
+        return q, out, lse
+    step_of(context(128, torch.bfloat16, 64, 1, 1, 1), False)
+    small = context(128)
+    small.track_weights()
+    q, out, lse = step_of(small, warm)
+    loaded = set()
+    for m in modules.values():
+        n = ok(cu.cuModuleGetFunctionCount(m))
+        for f in ok(cu.cuModuleEnumerateFunctions(n, m)):
+            if ok(cu.cuFuncIsLoaded(f)) == cu.CUfunctionLoadingState.CU_FUNCTION_LOADING_STATE_LOADED:
+                loaded.add(name(f))
+    big = context(longest)
+    big.track_weights()
+    used, apart = [], 0.0
+    for acc in (False, True):
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        graph = capture(big, q, o, l, acc)
+        used += [name(f) for f in functions(graph)]
+        run = ok(cu.cuGraphInstantiate(graph, 0))
+        assert cu.cuGraphLaunch(run, side.cuda_stream)[0] == cu.CUresult.CUDA_SUCCESS
+        side.synchronize()
+        w, _ = big.decode_attention(q, accumulate=acc)
+        side.synchronize()
+        apart = max(apart, float((o - w).abs().max()))
+    small.sync(); big.sync()
+print(json.dumps(dict(used=used, missing=[k for k in used if k not in loaded], apart=apart, top=float(w.abs().max()))))
+"""
+
+
+@pytest.mark.parametrize("case", [("int4", 128, 4, 2, 32768, 2, False), ("int4", 128, 8, 70, 32768, 8, False),
+                                  ("int4", 64, 4, 2, 32768, 2, True), ("bfloat16", 128, 4, 2, 32768, 2, False),
+                                  ("float32", 64, 2, 3, 32768, 2, True)], ids=str)
+def test_a_capture_meets_no_kernel_that_the_call_left_unloaded(case):
+    code = FRESH.format(paths=[os.path.dirname(HERE)], case=case)
+    env = dict(os.environ, CUDA_MODULE_LOADING="LAZY")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, env=env)
+    assert run.returncode == 0, run.stderr[-3000:]
+    got = json.loads(run.stdout.splitlines()[-1])
+    print(got)
+    assert got["used"] and not got["missing"]
+    assert got["apart"] <= 1e-5 * got["top"]
