@@ -897,7 +897,7 @@ kvc_status kvc_decode_attention_ex(kvc_ctx *ctx, int32_t layer_begin, int32_t la
   if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(ctx, KVC_ERR_INVALID_ARG, "scale must be finite and >= 0");
   const kvc_attention_options o = opts ? *opts : kvc_attention_options{0, 1.f, {0, 0}};
   if (o.accumulate != 0 && o.accumulate != 1) return fail(ctx, KVC_ERR_INVALID_ARG, "accumulate must be 0 or 1");
-  if (!(o.decay >= 0.f && o.decay <= 1.f)) return fail(ctx, KVC_ERR_INVALID_ARG, "decay must be in [0, 1]");
+  if (o.accumulate && !(o.decay >= 0.f && o.decay <= 1.f)) return fail(ctx, KVC_ERR_INVALID_ARG, "decay must be in [0, 1]");
   if (o.reserved[0] || o.reserved[1]) return fail(ctx, KVC_ERR_INVALID_ARG, "reserved option fields must be 0");
   if (o.accumulate && !ctx->weights)
     return fail(ctx, KVC_ERR_STATE, "accumulating needs tracked weights (call kvc_bind_weights)");

@@ -62,3 +62,16 @@ def test_seeded_loops(seed):
     run_step(ctx, rows(R, layers, H * G, d, 60 * seed, dtype=ctx.dtype)[0], list(range(layers)))
     assert isinstance(ctx.weights, torch.Tensor)
     ctx.close()
+
+
+def test_decay_is_ignored_without_accumulate():
+    """As the header says: any decay, a NaN among them, beside accumulate = 0."""
+    ctx = make([40], H=2, G=2, d=64)
+    fill(ctx, [40], seed=1)
+    q = rows(1, 1, 4, 64, 2)[0]
+    want = ctx.decode_attention(q)
+    for decay in (-1.0, 7.0, float("nan"), float("inf")):
+        got = ctx.decode_attention(q, decay=decay)
+        ctx.sync()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ctx.close()
