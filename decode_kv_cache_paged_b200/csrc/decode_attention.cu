@@ -16,7 +16,9 @@
 // CUDA cores and spends its effort on keeping HBM busy.
 //   * Work unit = (layer, request, KV head, split of the pages); one CTA of
 //     4 warps each.  Splits give short batches enough CTAs; a second kernel
-//     merges the per-split (max, sum, output) partials.
+//     merges the per-split (max, sum, output) partials.  The pages of a split
+//     follow from the longest request of the call, or, captured, from each
+//     request's length at the replay.
 //   * Each warp walks every 4th page of the unit on its own: the K rows and
 //     the V rows of a page are each 16 consecutive pool rows, so one bulk
 //     copy apiece (a contiguous 4 KB at bf16 d = 128) brings them into the

@@ -64,13 +64,13 @@ namespace kvc {
 namespace {
 
 constexpr size_t kMaxSmem = 227 * 1024 - 4608;  // the most for one, less the static shared memory
-constexpr int kPair = 2;    // pages per slot
+constexpr int kPair = 2;    // pages per slot: K, V of the first, K, V of the second
+constexpr int kStages = 2;  // slots per warp
 
 template <int D>
 struct Shape4 {
   static constexpr int kRow = int4_row_bytes(D);
   static constexpr int kPageBytes = kPage * kRow;       // K (or V) of one page
-  static constexpr int kSlot = kPair * 2 * kPageBytes;  // K, V of the first page, K, V of the second
   static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and K row
   static constexpr int kTiles = D / 16;  // products per page on the V side
 };
@@ -154,10 +154,10 @@ enum Mode4 { kStep, kStepWeights, kWeights };
 template <int GP, Mode4 MODE, int W>
 constexpr int kFit4 = (GP == 8 && MODE != kWeights ? 12 : 16) / W;  // CTAs whose registers fit an SM
 
-template <int D, int GP, Mode4 MODE, int W, int ST>
+template <int D, int GP, Mode4 MODE, int W>
 __global__ void __launch_bounds__(32 * W, kFit4<GP, MODE, W>) decode_attention4_kernel(DecodeAttnParams p, int G) {
   using S = Shape4<D>;
-  constexpr int kWarps = W, kThreads = 32 * W, kStages = ST;
+  constexpr int kWarps = W, kThreads = 32 * W;
   constexpr bool kValues = MODE != kWeights;
   constexpr int kYStride = (kValues ? 2 : 1) * S::kPageBytes;  // from a page of a slot to the next
   constexpr int kSlot = kPair * kYStride;
@@ -703,24 +703,24 @@ struct ClusterRule {
 };
 
 // shared memory of the page slots
-template <int D, Mode4 MODE, int W, int ST>
-constexpr size_t kRing4 = 128 + (size_t)W * ST * kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
+template <int D, Mode4 MODE, int W>
+constexpr size_t kRing4 = 128 + (size_t)W * kStages * kPair * (MODE == kWeights ? 1 : 2) * Shape4<D>::kPageBytes;
 
-template <int D, int GP, Mode4 MODE, int W, int ST>
+template <int D, int GP, Mode4 MODE, int W>
 cudaError_t launch4_w(DecodeAttnParams p, int G, AttnPages np, int sms, cudaStream_t s) {
-  auto kernel = decode_attention4_kernel<D, GP, MODE, W, ST>;
+  auto kernel = decode_attention4_kernel<D, GP, MODE, W>;
   p.part_o = p.part_ml = nullptr;
   return launch_attn_cluster(reinterpret_cast<const void *>(kernel), p, G, np, sms, kFit4<GP, MODE, W>,
-                             kRing4<D, MODE, W, ST>, MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W,
+                             kRing4<D, MODE, W>, MODE == kStepWeights ? (size_t)kPage * G * 4 : 0, 32 * W,
                              MODE != kWeights, s);
 }
 
 // A unit split over `splits` CTAs that are no cluster, and a launch that merges them.
 template <int D, int GP, int W>
 cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s) {
-  auto kernel = decode_attention4_kernel<D, GP, kStep, W, 2>;
+  auto kernel = decode_attention4_kernel<D, GP, kStep, W>;
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
-  const size_t smem = kRing4<D, kStep, W, 2>;
+  const size_t smem = kRing4<D, kStep, W>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   p.nsplit = splits;
@@ -731,11 +731,12 @@ cudaError_t launch4_split(DecodeAttnParams p, int G, int splits, cudaStream_t s)
 }
 
 // The step without weights.
-//   * With units enough to give every warp slot of the GPU one and a half, a
-//     unit is one warp's: no merge, and the start and end of a unit cost a
-//     quarter of what four warps pay (2048 rows, 4096 units: 272 us against
-//     290; 1024 units: 109 against 83).  A captured launch keeps the form over
-//     longer rows (4096 units of 8192 rows 1038 us, clusters 1069).
+//   * With 24 units an SM (one and a half for each of its 16 warp slots, two for
+//     each of 12 with 8 query heads), a unit is one warp's: no merge, and the
+//     start and end of a unit cost a quarter of what four warps pay (2048 rows,
+//     4096 units: 272 us against 290; 1024 units: 109 against 83).  A captured
+//     launch keeps the form over longer rows (4096 units of 8192 rows 1038 us,
+//     clusters 1069).
 //   * A few long requests are split without a cluster: the SMs take at most
 //     seven clusters of 16 with a CTA each, so that clusters share SMs while
 //     others idle (8 units of 32768 rows: 23 us against 35).
@@ -751,14 +752,14 @@ template <int D, int GP>
 cudaError_t launch4_step(const DecodeAttnParams &p, int G, AttnPages np, int sms, cudaStream_t s) {
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   if (units * 2 >= 16LL * sms * 3 && np.now <= 512)
-    return launch4_w<D, GP, kStep, 1, 2>(p, G, AttnPages{np.now, np.now}, sms, s);
+    return launch4_w<D, GP, kStep, 1>(p, G, AttnPages{np.now, np.now}, sms, s);
   const int splits = std::min({p.max_splits, (np.most + 15) / 16, (int)(2LL * sms / units)});
   if (splits > 8 && np.most >= 16 * splits) return launch4_split<D, GP, 8>(p, G, splits, s);
-  const int cs = ClusterRule{units, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4, 2>, 0}(np);
+  const int cs = ClusterRule{units, sms, 4, kFit4<GP, kStep, 4>, kRing4<D, kStep, 4>, 0}(np);
   const int parts = std::min(cs, p.max_splits);
   if (parts >= 4 && 2 * parts > cs && units * parts > (int64_t)kFit4<GP, kStep, 4> * sms)
     return launch4_split<D, GP, 4>(p, G, parts, s);
-  return launch4_w<D, GP, kStep, 4, 2>(p, G, np, sms, s);
+  return launch4_w<D, GP, kStep, 4>(p, G, np, sms, s);
 }
 
 // With weights the scores stay in shared memory unless a CTA of the largest
@@ -777,22 +778,22 @@ cudaError_t launch4(const DecodeAttnParams &p, int G, AttnPages np, int sms, cud
   const size_t keep = (size_t)kPage * G * 4 * ((np.most + 15) / 16);
   const int64_t units = (int64_t)p.layer_count * p.R * p.hkv;
   const size_t most = (units >= 384 ? 11 : units >= 128 ? 20 : 36) * 1024;
-  if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4, 2>(p, G, np, sms, s);
+  if (!p.lse2 || keep <= most) return launch4_w<D, GP, kStepWeights, 4>(p, G, np, sms, s);
   DecodeAttnParams step = p;
   step.weights = nullptr;
   if (cudaError_t e = launch4_step<D, GP>(step, G, np, sms, s)) return e;
-  return launch4_w<D, GP, kWeights, 4, 2>(p, G, np, sms, s);
+  return launch4_w<D, GP, kWeights, 4>(p, G, np, sms, s);
 }
 
 // Loads every form that launch4 may choose.
 template <int D, int GP>
 cudaError_t load4() {
   cudaFuncAttributes a;
-  for (const void *kernel : {reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 1, 2>),
-                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 4, 2>),
-                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 8, 2>),
-                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStepWeights, 4, 2>),
-                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kWeights, 4, 2>)})
+  for (const void *kernel : {reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 1>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 4>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStep, 8>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kStepWeights, 4>),
+                             reinterpret_cast<const void *>(decode_attention4_kernel<D, GP, kWeights, 4>)})
     if (cudaError_t e = cudaFuncGetAttributes(&a, kernel)) return e;
   return cudaSuccess;
 }
