@@ -77,13 +77,15 @@ struct AttnMerge {
 // 64-byte run) and starts the reads of kBatch such quads before the first is
 // used: one after the other the loop waits for memory once per quad, which
 // cost a third of the step at 2048 rows.
-template <int NT, int G>
+template <int NT, int G, bool KEEP_NAN>
 __device__ __forceinline__ void attn_add_weights(const DecodeAttnParams &p, const AttnUnit &u,
                                                  const float (&lse2)[8], const float *scores) {
   constexpr int kBatch = 4;
   const int rows = min(u.len, u.pg1 * kPage) - u.pg0 * kPage;
   float *w0 = p.weights + ((int64_t)u.l * p.num_pages * p.hkv + u.h) * kPage;
   const int64_t page_stride = (int64_t)p.hkv * kPage;
+  // a head that reads as one without rows has lse2 = +inf: its finite scores give 0, the others NaN, which max drops
+  auto weight = [](float s) { return KEEP_NAN ? attn_ex2(s) : fmaxf(attn_ex2(s), 0.f); };
   for (int j0 = threadIdx.x * 4; j0 < rows; j0 += 4 * NT * kBatch) {
     float4 w[kBatch];
     float *at[kBatch];
@@ -104,10 +106,10 @@ __device__ __forceinline__ void attn_add_weights(const DecodeAttnParams &p, cons
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float4 v = *reinterpret_cast<const float4 *>(sc + g * kPage);
-        a.x += attn_ex2(v.x - lse2[g]);
-        a.y += attn_ex2(v.y - lse2[g]);
-        a.z += attn_ex2(v.z - lse2[g]);
-        a.w += attn_ex2(v.w - lse2[g]);
+        a.x += weight(v.x - lse2[g]);
+        a.y += weight(v.y - lse2[g]);
+        a.z += weight(v.z - lse2[g]);
+        a.w += weight(v.w - lse2[g]);
       }
       a = make_float4(fmaf(p.decay, w[b].x, a.x), fmaf(p.decay, w[b].y, a.y), fmaf(p.decay, w[b].z, a.z),
                       fmaf(p.decay, w[b].w, a.w));
@@ -224,21 +226,11 @@ __device__ __forceinline__ void attn_finish(const DecodeAttnParams &p, const Att
     float lse2[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) lse2[x] = x < G ? mg.lse2[x] : 0.f;
-    if constexpr (!KEEP_NAN) {  // heads that read as ones without rows: no score of theirs counts
-      float top = lse2[0];
-#pragma unroll
-      for (int x = 1; x < 8; ++x) top = fmaxf(top, lse2[x]);
-      if (top == INFINITY) {
-        for (int i = tid; i < (u.pg1 - u.pg0) * kPage * G; i += NT)
-          if (mg.lse2[i / kPage % G] == INFINITY) scores[i] = -INFINITY;
-        __syncthreads();
-      }
-    }
     switch (G) {
-      case 1: attn_add_weights<NT, 1>(p, u, lse2, scores); break;
-      case 2: attn_add_weights<NT, 2>(p, u, lse2, scores); break;
-      case 4: attn_add_weights<NT, 4>(p, u, lse2, scores); break;
-      default: attn_add_weights<NT, 8>(p, u, lse2, scores);
+      case 1: attn_add_weights<NT, 1, KEEP_NAN>(p, u, lse2, scores); break;
+      case 2: attn_add_weights<NT, 2, KEEP_NAN>(p, u, lse2, scores); break;
+      case 4: attn_add_weights<NT, 4, KEEP_NAN>(p, u, lse2, scores); break;
+      default: attn_add_weights<NT, 8, KEEP_NAN>(p, u, lse2, scores);
     }
   }
   if (u.cs > 1) cluster_sync_all();  // the others may still read this CTA's shared memory
