@@ -110,6 +110,37 @@ def test_replays_follow_the_lengths(first, then, cache, accumulate):
     ctx.close()
 
 
+@pytest.mark.parametrize("accumulate", [False, True], ids=["step", "weights"])
+def test_many_units_captured_over_an_empty_cache(accumulate):
+    """Units enough for the form with one warp a unit, captured before any row is there."""
+    R, layers, H, G, d = 64, 7, 8, 2, 64
+    then = [(37 * i) % 900 for i in range(R - 1)] + [6000]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ctx = Context(ContextSpec(num_requests=R, num_layers=layers, num_kv_heads=H, head_dim=d, max_seq_len=32768,
+                                  num_pages=4096, num_q_heads=H * G), dtype="int4")
+        if accumulate:
+            ctx.track_weights()
+        q = rows(R, layers, H * G, d, 41, dtype=ctx.dtype)[0]
+        out, lse = ctx.decode_attention(q, accumulate=accumulate)
+        side.synchronize()
+        assert not out.any() and torch.isneginf(lse).all()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            ctx.decode_attention(q, out=out, lse=lse, accumulate=accumulate)
+        fill(ctx, then, seed=42)
+        graph.replay()
+        side.synchronize()
+        for layer in (0, layers - 1):
+            check_attention(ctx, q[layer:layer + 1], out[layer:layer + 1], lse[layer:layer + 1], [layer], d ** -0.5)
+            if accumulate:
+                none = {layer: torch.zeros((R, H, max(then)), device="cuda")}
+                check_weights(ctx, q[layer:layer + 1], none, [layer], d ** -0.5, 1.0)
+        side.synchronize()
+        del graph
+    ctx.close()
+
+
 # One short call, then a capture whose longest rows may be 32768, in a process that has loaded nothing before.  Prints the
 # kernels of the capture and those of them that the call had not loaded, and the largest difference from a call's outputs.
 FRESH = r"""
