@@ -323,13 +323,15 @@ kvc_status kvc_compress_ex(kvc_ctx *ctx, kvc_selector selector, const int32_t *b
  *     s_j = scale * q . k_j over the request's cached rows j < length(r),
  *     out = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j).
  * Slot order does not matter (rows after hole filling included).  A request
- * with no rows gets out = 0 and lse = -inf.  So does a head with a NaN or
- * +infinite score, or with none above -infinity (a score of -infinity has
- * weight 0), whether or not the step accumulates weights; a NaN in a value
- * shows in its output.  Over a KVC_INT4 cache a NaN score shows as NaN in the
- * head's out and lse, and in the weights of a step that accumulates them.
+ * with no rows gets out = 0 and lse = -inf.  Over a KVC_BF16 or KVC_F32 cache
+ * so does a head with a NaN or +infinite score, or with none above -infinity
+ * (a score of -infinity has weight 0), whether or not the step accumulates
+ * weights; a NaN in a value shows in its output.
  * Over a KVC_INT4 cache k_j and v_j are the values that the codes stand for,
- * and the queries and values are to stay below 2^100 in size.
+ * the queries and values are to stay below 2^100 in size and their scores
+ * finite in fp32.  A NaN score (a broken group, a NaN or infinite query) shows
+ * as NaN in the head's out and lse, and in the weights of a step that
+ * accumulates them.
  *   q:   device [layer_count][num_requests][num_q_heads][head_dim] in the
  *        cache dtype (bf16 for KVC_INT4), element-aligned; read only.
  *   scale: > 0, or 0 for 1/sqrt(head_dim).
@@ -359,9 +361,9 @@ kvc_status kvc_decode_attention(kvc_ctx *ctx, int32_t layer_begin, int32_t layer
  *     every row j < length(r) of the listed layers and each KV head h,
  *         w_j <- decay * w_j + sum over the G query heads g of h of
  *                              exp(s_gj - lse_g).
- *     A step adds G per (request, layer, KV head) in all, less 1 for each
- *     head that reads as one without rows (kvc_decode_attention): it adds
- *     none.  Rows past a request's length are left as they are.
+ *     A step adds G per (request, layer, KV head) in all; a head that reads
+ *     as one without rows (kvc_decode_attention) adds none.  Rows past a
+ *     request's length are left as they are.
  *   decay: in [0, 1]; 1 gives the plain sum over the steps, 0 the last step's
  *     weights (where they were finite: decay * w_j is a product like any
  *     other).  Ignored without accumulate.
